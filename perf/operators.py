@@ -36,7 +36,7 @@ def listed():
                   norm=True, far=131072))
     # a prefill batch of an odd token count, rotation over half of each head in
     # neighbouring pairs, no norm
-    c.append(dict(name="norm-rope 4093 tokens, pairs", op="qk_norm_rope", tokens=4093, hq=32, hkv=8, d=128, rot=64,
+    c.append(dict(name="norm-rope 4093 tokens pairs", op="qk_norm_rope", tokens=4093, hq=32, hkv=8, d=128, rot=64,
                   pairs=True, norm=False, far=8192))
     # 64 prompts of 2048 tokens
     c.append(dict(name="norm-rope 131072 tokens", op="qk_norm_rope", tokens=131072, hq=32, hkv=8, d=128, rot=128,
@@ -63,7 +63,7 @@ def listed():
                   lq=1, hq=32, hkv=8, d=128, page=PAGE, fp8=False, lens=6))
     # four prompts of different lengths, 16 samples each, four drafted tokens
     # a sequence (causal among them), head dim 64, six heads a group
-    c.append(dict(name="shared-prefix 4 groups, drafts", op="shared_prefix", groups=4, seqs=16, prefix=6000,
+    c.append(dict(name="shared-prefix 4 groups drafts", op="shared_prefix", groups=4, seqs=16, prefix=6000,
                   own_max=700, lq=4, hq=12, hkv=2, d=64, page=PAGE, fp8=False, lens=7))
     # e4m3 cache
     c.append(dict(name="shared-prefix 64 x 8192 fp8", op="shared_prefix", groups=1, seqs=64, prefix=8192, own_max=1024,
