@@ -302,6 +302,92 @@ pkv_status pkv_get_status_noalloc(void* stream, int32_t* device_status);
 pkv_status pkv_kv_append(const pkv_problem* problem, const pkv_fwd_args* args,
                          int32_t total_new, int32_t* device_status, void* stream);
 
+/*
+ * How rows of queries and keys are normed and rotated before they reach the
+ * cache or the attention (the step that every model with rotary positions runs
+ * first).  For a row x of head_dim values, all in fp32:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      (weight given; else y = x)
+ *   for i < rot_dim / 2, with c, s = cos, sin of the row's position and i:
+ *     (a, b) = (y[i], y[i + rot_dim/2])          (interleaved = 0)
+ *            = (y[2i], y[2i + 1])                (interleaved = 1)
+ *     (a, b) <- (a c - b s, b c + a s)
+ * dims from rot_dim on pass through; one rounding at the end (to bf16, or to
+ * the fp8 cache's code).
+ */
+typedef struct {
+  const float* cos_sin;    /* [num_positions, rot_dim] fp32, row p: rot_dim/2 cosines, then rot_dim/2
+                              sines, of position p; 16-byte aligned; NULL iff rot_dim = 0 (no rotation) */
+  int32_t num_positions;   /* rows of cos_sin                                    */
+  int32_t rot_dim;         /* rotated dims: a multiple of 8, <= head_dim, 0 = none */
+  int32_t interleaved;     /* 0 / 1: which dims form a pair (above)              */
+  float eps;               /* > 0 where a weight is given                        */
+  const void* q_weight;    /* nullable: [head_dim] bf16, 16-byte aligned         */
+  const void* k_weight;    /* nullable: likewise, for key rows                   */
+} pkv_rope_spec;
+
+/* Tensors of pkv_qk_norm_rope. */
+typedef struct {
+  int32_t num_tokens;      /* T                                                  */
+  int32_t num_heads_q;     /* heads of q (0 with q = NULL)                       */
+  int32_t num_heads_kv;    /* heads of k (0 with k = NULL)                       */
+  int32_t head_dim;        /* 64, 128 or 256                                     */
+  const void* q;           /* nullable; (T, Hq, D) bf16                          */
+  int64_t q_stride_tok, q_stride_head;
+  void* q_out;             /* (T, Hq, D) bf16, written; may be q itself (same strides) */
+  int64_t qo_stride_tok, qo_stride_head;
+  const void* k;           /* nullable; (T, Hkv, D) bf16                         */
+  int64_t k_stride_tok, k_stride_head;
+  void* k_out;             /* likewise                                           */
+  int64_t ko_stride_tok, ko_stride_head;
+  const int32_t* positions;/* [T], required iff rot_dim > 0                      */
+} pkv_qk_args;
+
+/*
+ * pkv_qk_norm_rope -- norm of every head of q and k and the rotation by each
+ * token's position, in one pass (pkv_rope_spec above); q_out and k_out are what
+ * pkv_attn_varlen_kvcache_fwd takes as q and k_new.  An output either is its
+ * input (in place, same strides) or does not overlap any input.  A token whose
+ * position is not in [0, num_positions) records PKV_ERR_DEVICE_BOUNDS and its
+ * rows are not written.  device_status: nullable device int32[3], zeroed by the
+ * caller: the first error code and two details.
+ */
+pkv_status pkv_qk_norm_rope(const pkv_qk_args* args, const pkv_rope_spec* spec,
+                            int32_t* device_status, void* stream);
+
+/* The rotating forms of the append and of the attention call. */
+typedef struct {
+  pkv_rope_spec spec;
+  void* q_out;             /* nullable; (total_q, Hq, D) bf16: the transformed queries; may be
+                              args->q itself (same strides)                      */
+  int64_t qo_stride_tok, qo_stride_head;
+} pkv_rope_append_args;
+
+/*
+ * pkv_rope_kv_append -- pkv_kv_append with the norm and rotation applied on the
+ * way: new token t of sequence b is rotated by its position in the cache,
+ * cache_seqlens[b] + t, and its key row written there (bf16, or the e4m3 code of
+ * the fp32 row times fp32(1/k_scale)); values are appended as they are.  With
+ * q_out, the queries args->q (packed by cu_seqlens_q, total_q rows) go there
+ * normed and rotated in the same launch; sequence b's Lq queries are the last Lq
+ * of its cache_seqlens[b] + new_len[b] positions.  total_q and total_new: host
+ * counts (either may be 0).  A row whose cache slot, page or table row is out of
+ * range is skipped and records PKV_ERR_DEVICE_BOUNDS in device_status (nullable
+ * device int32[3]).
+ */
+pkv_status pkv_rope_kv_append(const pkv_problem* problem, const pkv_fwd_args* args,
+                              const pkv_rope_append_args* rope, int32_t total_q, int32_t total_new,
+                              int32_t* device_status, void* stream);
+
+/*
+ * pkv_rope_attn_varlen_kvcache_fwd -- pkv_attn_varlen_kvcache_fwd with
+ * pkv_rope_kv_append in place of its append: queries and new keys come as the
+ * projection left them, and the attention reads rope->q_out (required when the
+ * plan has queries).  args->q_rows must be 0.
+ */
+pkv_status pkv_rope_attn_varlen_kvcache_fwd(const pkv_problem* problem, const pkv_fwd_args* args,
+                                            const pkv_rope_append_args* rope, pkv_plan_t plan,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, reads the device status word of `workspace` into
  * *device_status (a pkv_status) and resets it to PKV_OK. */
 pkv_status pkv_get_status(void* workspace, void* stream, int32_t* device_status);

@@ -26,7 +26,8 @@ STATUS_NAMES = {
 # every symbol the header declares
 EXPORTED = ["pkv_plan", "pkv_plan_upload", "pkv_plan_get_stats", "pkv_plan_get_items", "pkv_attn_varlen_kvcache_fwd", "pkv_kv_append",
             "pkv_get_status", "pkv_plan_destroy", "pkv_last_error", "pkv_version", "pkv_set_profile_events",
-            "pkv_attn_varlen_kvcache_fwd_noalloc", "pkv_plan_decode_dynamic", "pkv_get_status_noalloc"]
+            "pkv_attn_varlen_kvcache_fwd_noalloc", "pkv_plan_decode_dynamic", "pkv_get_status_noalloc",
+            "pkv_qk_norm_rope", "pkv_rope_kv_append", "pkv_rope_attn_varlen_kvcache_fwd"]
 
 
 class PkvError(RuntimeError):
@@ -53,6 +54,24 @@ class FwdArgs(ctypes.Structure):
                 ("cache_seqlens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("block_table_stride", ctypes.c_int32), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("page_indptr", ctypes.c_void_p), ("q_scale", ctypes.c_void_p), ("q_rows", ctypes.c_int32)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
+class QkArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "num_heads_q", "num_heads_kv", "head_dim")] + [
+        (n, ctypes.c_int64 if "stride" in n else ctypes.c_void_p)
+        for n in ("q", "q_stride_tok", "q_stride_head", "q_out", "qo_stride_tok", "qo_stride_head",
+                  "k", "k_stride_tok", "k_stride_head", "k_out", "ko_stride_tok", "ko_stride_head", "positions")]
+
+
+class RopeAppendArgs(ctypes.Structure):
+    _fields_ = [("spec", RopeSpec), ("q_out", ctypes.c_void_p), ("qo_stride_tok", ctypes.c_int64),
+                ("qo_stride_head", ctypes.c_int64)]
 
 
 class WorkItemInfo(ctypes.Structure):
@@ -93,13 +112,19 @@ def lib() -> ctypes.CDLL:
         L.pkv_set_profile_events.argtypes = [vp, vp]
         L.pkv_attn_varlen_kvcache_fwd_noalloc.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(FwdArgs), vp, vp]
         L.pkv_get_status_noalloc.argtypes = [vp, ctypes.POINTER(i32)]
+        L.pkv_qk_norm_rope.argtypes = [ctypes.POINTER(QkArgs), ctypes.POINTER(RopeSpec), vp, vp]
+        L.pkv_rope_kv_append.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(FwdArgs),
+                                         ctypes.POINTER(RopeAppendArgs), i32, i32, vp, vp]
+        L.pkv_rope_attn_varlen_kvcache_fwd.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(FwdArgs),
+                                                       ctypes.POINTER(RopeAppendArgs), vp, vp, sz, vp]
         L.pkv_plan_destroy.argtypes = [vp]
         L.pkv_plan_destroy.restype = None
         L.pkv_last_error.restype = ctypes.c_char_p
         L.pkv_version.restype = ctypes.c_char_p
         for name in ("pkv_plan", "pkv_plan_upload", "pkv_plan_get_stats", "pkv_plan_get_items", "pkv_attn_varlen_kvcache_fwd",
                      "pkv_kv_append", "pkv_get_status", "pkv_set_profile_events",
-                     "pkv_attn_varlen_kvcache_fwd_noalloc", "pkv_get_status_noalloc"):
+                     "pkv_attn_varlen_kvcache_fwd_noalloc", "pkv_get_status_noalloc", "pkv_qk_norm_rope",
+                     "pkv_rope_kv_append", "pkv_rope_attn_varlen_kvcache_fwd"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -165,6 +190,74 @@ def make_args(*, q, out, cu_seqlens_q, max_seqlen_q, k_cache, v_cache, cache_seq
     a.q_scale = _ptr(q_scale)
     a.q_rows = int(q_rows)
     return a
+
+
+def _need(t, what: str, dtypes: tuple, ndim: int) -> None:
+    """Raises ValueError unless t has one of the dtypes (by name), ndim dims and a unit innermost stride."""
+    if str(t.dtype).removeprefix("torch.") not in dtypes or t.dim() != ndim:
+        raise ValueError(f"{what}: {ndim}-d tensor of {' or '.join(dtypes)} expected, got {tuple(t.shape)} {t.dtype}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: innermost stride must be 1")
+
+
+def make_rope_spec(*, cos_sin=None, interleaved=False, eps=1e-6, q_weight=None, k_weight=None) -> RopeSpec:
+    """How rows are normed and rotated.  cos_sin: (positions, rot_dim) fp32, the
+    rot_dim/2 cosines and then sines of each position (None: no rotation);
+    q_weight / k_weight: (head_dim,) bf16 RMS norm weights (None: no norm)."""
+    r = RopeSpec(interleaved=int(bool(interleaved)), eps=eps, q_weight=_ptr(q_weight), k_weight=_ptr(k_weight))
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, what, ("bfloat16",), 1)
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", ("float32",), 2)
+        if cos_sin.shape[0] > 1 and cos_sin.stride(0) != cos_sin.shape[1]:
+            raise ValueError("cos_sin must be contiguous")
+        r.cos_sin, (r.num_positions, r.rot_dim) = cos_sin.data_ptr(), cos_sin.shape
+    return r
+
+
+def make_qk_args(*, q=None, k=None, positions=None, q_out=None, k_out=None) -> QkArgs:
+    """Tensors of ``qk_norm_rope``: q (T, Hq, D) and / or k (T, Hkv, D) bf16, int32
+    positions (T,), and where the results go (None: in place)."""
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    a = QkArgs()
+    t = q if q is not None else k
+    a.num_tokens, a.head_dim = t.shape[0], t.shape[-1]
+    if positions is not None:
+        _need(positions, "positions", ("int32",), 1)
+        if positions.shape[0] != a.num_tokens:
+            raise ValueError(f"positions: {a.num_tokens} tokens expected, got {positions.shape[0]}")
+        a.positions = positions.data_ptr()
+    for what, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{what}_out given without {what}")
+            continue
+        y = x if y is None else y
+        _need(x, what, ("bfloat16",), 3)
+        _need(y, what + "_out", ("bfloat16",), 3)
+        if x.shape != y.shape or x.shape[0] != a.num_tokens or x.shape[2] != a.head_dim:
+            raise ValueError(f"{what} {tuple(x.shape)} and {what}_out {tuple(y.shape)} must agree in shape, and q and k "
+                             "in tokens and head_dim")
+        setattr(a, "num_heads_q" if what == "q" else "num_heads_kv", x.shape[1])
+        setattr(a, what, x.data_ptr())
+        setattr(a, what + "_stride_tok", x.stride(0))
+        setattr(a, what + "_stride_head", x.stride(1))
+        setattr(a, what + "_out", y.data_ptr())
+        setattr(a, what + "o_stride_tok", y.stride(0))
+        setattr(a, what + "o_stride_head", y.stride(1))
+    return a
+
+
+def make_rope_append_args(*, spec: RopeSpec, q_out=None) -> RopeAppendArgs:
+    """The transform of ``rope_kv_append`` and where its queries go (None: the
+    queries are left alone)."""
+    r = RopeAppendArgs(spec=spec)
+    if q_out is not None:
+        _need(q_out, "q_out", ("bfloat16",), 3)
+        r.q_out, r.qo_stride_tok, r.qo_stride_head = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
+    return r
 
 
 class Plan:
@@ -252,6 +345,28 @@ def get_status_noalloc(stream=None) -> int:
 def kv_append(problem: Problem, args: FwdArgs, total_new: int, device_status=None, stream=None) -> None:
     _check(lib().pkv_kv_append(ctypes.byref(problem), ctypes.byref(args), int(total_new), _ptr(device_status),
                                _stream_handle(stream)))
+
+
+def qk_norm_rope(args: QkArgs, spec: RopeSpec, device_status=None, stream=None) -> None:
+    """Norm of every head of q and k and the rotation by each token's position, in one pass."""
+    _check(lib().pkv_qk_norm_rope(ctypes.byref(args), ctypes.byref(spec), _ptr(device_status),
+                                  _stream_handle(stream)))
+
+
+def rope_kv_append(problem: Problem, args: FwdArgs, rope: RopeAppendArgs, total_q: int, total_new: int,
+                   device_status=None, stream=None) -> None:
+    """``kv_append`` with the norm and rotation on the way into the cache, and of the queries into rope's q_out."""
+    _check(lib().pkv_rope_kv_append(ctypes.byref(problem), ctypes.byref(args), ctypes.byref(rope), int(total_q),
+                                    int(total_new), _ptr(device_status), _stream_handle(stream)))
+
+
+def rope_attn_varlen_kvcache_fwd(problem: Problem, args: FwdArgs, rope: RopeAppendArgs, plan_: Plan, workspace,
+                                 stream=None) -> None:
+    """The attention call with ``rope_kv_append`` in place of its append."""
+    _check(lib().pkv_rope_attn_varlen_kvcache_fwd(ctypes.byref(problem), ctypes.byref(args), ctypes.byref(rope),
+                                                  plan_.handle, workspace.data_ptr(),
+                                                  workspace.numel() * workspace.element_size(),
+                                                  _stream_handle(stream)))
 
 
 def get_status(workspace, stream=None) -> int:

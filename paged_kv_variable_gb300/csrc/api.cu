@@ -2,6 +2,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -168,6 +169,98 @@ AppendParams append_params(const pkv_problem& pr, const pkv_fwd_args* a, int32_t
   return ap;
 }
 
+pkv_status validate_rope_spec(const pkv_rope_spec& r, int head_dim) {
+  if (r.rot_dim < 0 || r.rot_dim > head_dim || r.rot_dim % 8 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "rot_dim %d: a multiple of 8 from 0 to head_dim", r.rot_dim);
+  if ((r.rot_dim > 0) != (r.cos_sin != nullptr))
+    return fail(PKV_ERR_INVALID_ARG, "cos_sin must be given exactly when rot_dim > 0");
+  if (r.rot_dim > 0 && (r.num_positions <= 0 || !aligned16(r.cos_sin)))
+    return fail(PKV_ERR_INVALID_ARG, "cos_sin needs num_positions > 0 and a 16-byte aligned base");
+  if (r.interleaved != 0 && r.interleaved != 1) return fail(PKV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if ((r.q_weight && !aligned16(r.q_weight)) || (r.k_weight && !aligned16(r.k_weight)))
+    return fail(PKV_ERR_INVALID_ARG, "norm weights must be 16-byte aligned");
+  if ((r.q_weight || r.k_weight) && !(std::isfinite(r.eps) && r.eps > 0.f))
+    return fail(PKV_ERR_INVALID_ARG, "eps must be finite and positive");
+  return PKV_OK;
+}
+
+// One bf16 tensor of head rows (tokens, heads, head_dim): base and strides.
+pkv_status validate_rows(const char* what, const void* ptr, int64_t stride_tok, int64_t stride_head, int head_dim) {
+  if (!ptr) return fail(PKV_ERR_INVALID_ARG, "%s is NULL", what);
+  if (!aligned16(ptr) || stride_head < head_dim || stride_tok <= 0 || stride_head % 8 || stride_tok % 8)
+    return fail(PKV_ERR_INVALID_ARG,
+                "%s must be 16-byte aligned, with strides that are multiples of 8 elements (heads: >= head_dim)", what);
+  return PKV_OK;
+}
+
+// An output is its own input (same strides) or, as far as their first elements
+// show, another tensor.
+pkv_status validate_in_place(const char* what, const void* in, const void* out, int64_t it, int64_t ih, int64_t ot,
+                             int64_t oh) {
+  if (in == out && (it != ot || ih != oh))
+    return fail(PKV_ERR_INVALID_ARG, "%s in place needs the strides of its input", what);
+  return PKV_OK;
+}
+
+RopeParams rope_params(const pkv_rope_spec& r) {
+  RopeParams rp{};
+  rp.cos_sin = r.cos_sin;
+  rp.num_positions = r.num_positions;
+  rp.rot_dim = r.rot_dim;
+  rp.interleaved = r.interleaved;
+  rp.eps = r.eps;
+  rp.q_weight = static_cast<const __nv_bfloat16*>(r.q_weight);
+  rp.k_weight = static_cast<const __nv_bfloat16*>(r.k_weight);
+  return rp;
+}
+
+// Host checks of the rotating append (the problem has passed its own).
+pkv_status validate_rope_append(const pkv_problem& pr, const pkv_fwd_args* a, const pkv_rope_append_args* r,
+                                int32_t total_q, int32_t total_new) {
+  pkv_status st = validate_cache_args(pr, a);
+  if (st != PKV_OK) return st;
+  if (!r) return fail(PKV_ERR_INVALID_ARG, "rope arguments are NULL");
+  st = validate_rope_spec(r->spec, pr.head_dim);
+  if (st != PKV_OK) return st;
+  if (total_q < 0 || total_new < 0) return fail(PKV_ERR_INVALID_ARG, "total_q or total_new < 0");
+  if (pr.batch == 0 && (total_q > 0 || total_new > 0)) return fail(PKV_ERR_INVALID_ARG, "tokens given for batch 0");
+  if (total_new > 0) {
+    st = validate_new_args(pr, a);
+    if (st != PKV_OK) return st;
+  }
+  if (total_q > 0 && r->q_out) {
+    if (!a->cu_seqlens_q) return fail(PKV_ERR_INVALID_ARG, "cu_seqlens_q is NULL");
+    if (a->q_rows != 0) return fail(PKV_ERR_UNSUPPORTED, "the rotating append takes packed query rows (q_rows = 0)");
+    st = validate_rows("q", a->q, a->q_stride_tok, a->q_stride_head, pr.head_dim);
+    if (st != PKV_OK) return st;
+    st = validate_rows("q_out", r->q_out, r->qo_stride_tok, r->qo_stride_head, pr.head_dim);
+    if (st != PKV_OK) return st;
+    st = validate_in_place("q_out", a->q, r->q_out, a->q_stride_tok, a->q_stride_head, r->qo_stride_tok,
+                           r->qo_stride_head);
+    if (st != PKV_OK) return st;
+  }
+  return PKV_OK;
+}
+
+cudaError_t run_rope_append(const pkv_problem& pr, const pkv_fwd_args* a, const pkv_rope_append_args* r,
+                            int32_t total_q, int32_t total_new, int* status, cudaStream_t s) {
+  RopeParams rp = rope_params(r->spec);
+  rp.a = append_params(pr, a, total_new, status);
+  rp.cu_q = a->cu_seqlens_q;
+  if (total_q > 0 && r->q_out) {
+    rp.q = static_cast<const __nv_bfloat16*>(a->q);
+    rp.q_stride_tok = a->q_stride_tok;
+    rp.q_stride_head = a->q_stride_head;
+    rp.q_out = static_cast<__nv_bfloat16*>(r->q_out);
+    rp.qo_stride_tok = r->qo_stride_tok;
+    rp.qo_stride_head = r->qo_stride_head;
+    rp.total_q = total_q;
+    rp.hq = pr.num_heads_q;
+  }
+  if (total_new == 0) rp.a.hkv = 0;
+  return launch_rope_kv_append(rp, pr.head_dim, pr.cache_dtype == PKV_FP8_E4M3, s);
+}
+
 bool same_problem(const pkv_problem& x, const pkv_problem& y) {
   return x.batch == y.batch && x.num_heads_q == y.num_heads_q && x.num_heads_kv == y.num_heads_kv &&
          x.head_dim == y.head_dim && x.page_size == y.page_size && x.cache_capacity == y.cache_capacity &&
@@ -213,6 +306,71 @@ extern "C" pkv_status pkv_kv_append(const pkv_problem* problem, const pkv_fwd_ar
   return PKV_OK;
 }
 
+extern "C" pkv_status pkv_qk_norm_rope(const pkv_qk_args* args, const pkv_rope_spec* spec, int32_t* device_status,
+                                       void* stream) {
+  if (!args || !spec) return fail(PKV_ERR_INVALID_ARG, "args or spec is NULL");
+  const pkv_qk_args& a = *args;
+  if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256)
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %d not in {64, 128, 256}", a.head_dim);
+  pkv_status st = validate_rope_spec(*spec, a.head_dim);
+  if (st != PKV_OK) return st;
+  if (a.num_tokens < 0 || a.num_heads_q < 0 || a.num_heads_kv < 0)
+    return fail(PKV_ERR_INVALID_ARG, "negative token or head count");
+  if ((a.num_heads_q > 0) != (a.q != nullptr) || (a.num_heads_kv > 0) != (a.k != nullptr))
+    return fail(PKV_ERR_INVALID_ARG, "heads without a tensor, or a tensor without heads");
+  if (a.num_tokens == 0 || (a.num_heads_q == 0 && a.num_heads_kv == 0)) return PKV_OK;
+  if (spec->rot_dim > 0 && !a.positions) return fail(PKV_ERR_INVALID_ARG, "positions is NULL");
+  if (a.q) {
+    st = validate_rows("q", a.q, a.q_stride_tok, a.q_stride_head, a.head_dim);
+    if (st == PKV_OK) st = validate_rows("q_out", a.q_out, a.qo_stride_tok, a.qo_stride_head, a.head_dim);
+    if (st == PKV_OK)
+      st = validate_in_place("q_out", a.q, a.q_out, a.q_stride_tok, a.q_stride_head, a.qo_stride_tok, a.qo_stride_head);
+    if (st != PKV_OK) return st;
+  }
+  if (a.k) {
+    st = validate_rows("k", a.k, a.k_stride_tok, a.k_stride_head, a.head_dim);
+    if (st == PKV_OK) st = validate_rows("k_out", a.k_out, a.ko_stride_tok, a.ko_stride_head, a.head_dim);
+    if (st == PKV_OK)
+      st = validate_in_place("k_out", a.k, a.k_out, a.k_stride_tok, a.k_stride_head, a.ko_stride_tok, a.ko_stride_head);
+    if (st != PKV_OK) return st;
+  }
+  RopeParams rp = rope_params(*spec);
+  rp.q = static_cast<const __nv_bfloat16*>(a.q);
+  rp.q_stride_tok = a.q_stride_tok;
+  rp.q_stride_head = a.q_stride_head;
+  rp.q_out = static_cast<__nv_bfloat16*>(a.q_out);
+  rp.qo_stride_tok = a.qo_stride_tok;
+  rp.qo_stride_head = a.qo_stride_head;
+  rp.total_q = a.q ? a.num_tokens : 0;
+  rp.hq = a.num_heads_q;
+  rp.positions = a.positions;
+  rp.a.k_new = static_cast<const __nv_bfloat16*>(a.k);
+  rp.a.n_stride_tok = a.k_stride_tok;
+  rp.a.n_stride_head = a.k_stride_head;
+  rp.a.k_cache = a.k_out;
+  rp.a.c_stride_tok = a.ko_stride_tok;
+  rp.a.c_stride_head = a.ko_stride_head;
+  rp.a.total_new = a.k ? a.num_tokens : 0;
+  rp.a.hkv = a.num_heads_kv;
+  rp.a.status = reinterpret_cast<int*>(device_status);
+  cudaError_t e = launch_qk_norm_rope(rp, a.head_dim, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope launch");
+  return PKV_OK;
+}
+
+extern "C" pkv_status pkv_rope_kv_append(const pkv_problem* problem, const pkv_fwd_args* args,
+                                         const pkv_rope_append_args* rope, int32_t total_q, int32_t total_new,
+                                         int32_t* device_status, void* stream) {
+  pkv_status st = validate_problem(problem);
+  if (st != PKV_OK) return st;
+  st = validate_rope_append(*problem, args, rope, total_q, total_new);
+  if (st != PKV_OK) return st;
+  cudaError_t e = run_rope_append(*problem, args, rope, total_q, total_new, reinterpret_cast<int*>(device_status),
+                                  static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_kv_append launch");
+  return PKV_OK;
+}
+
 namespace pkv {
 
 // Every host-side check of an attention call that does not involve the
@@ -255,11 +413,20 @@ pkv_status validate_call(const pkv_problem* problem, const pkv_fwd_args* args, p
 
 }  // namespace pkv
 
-extern "C" pkv_status pkv_attn_varlen_kvcache_fwd(const pkv_problem* problem, const pkv_fwd_args* args,
-                                                  pkv_plan_t plan, void* workspace, size_t workspace_bytes,
-                                                  void* stream) {
+namespace pkv {
+namespace {
+
+// The whole call: append (with a rotation, if `rope` is given), attention, combine.
+pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const pkv_rope_append_args* rope,
+                    pkv_plan_t plan, void* workspace, size_t workspace_bytes, void* stream) {
   pkv_status st = validate_call(problem, args, plan);
   if (st != PKV_OK) return st;
+  pkv_fwd_args rotated;
+  if (rope) {
+    st = validate_rope_append(*problem, args, rope, plan->total_q, plan->total_new);
+    if (st != PKV_OK) return st;
+    if (plan->total_q > 0 && !rope->q_out) return fail(PKV_ERR_INVALID_ARG, "q_out is NULL");
+  }
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
     return fail(PKV_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
   if (workspace_bytes < plan->layout.total)
@@ -269,7 +436,16 @@ extern "C" pkv_status pkv_attn_varlen_kvcache_fwd(const pkv_problem* problem, co
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   int* status = reinterpret_cast<int*>(ws + plan->layout.status);
 
-  if (plan->total_new > 0) {
+  if (rope) {
+    cudaError_t e = run_rope_append(pr, args, rope, plan->total_q, plan->total_new, status, s);
+    if (e != cudaSuccess) return cuda_fail(e, "rope_kv_append launch");
+    // the attention reads the transformed queries
+    rotated = *args;
+    rotated.q = rope->q_out;
+    rotated.q_stride_tok = rope->qo_stride_tok;
+    rotated.q_stride_head = rope->qo_stride_head;
+    args = &rotated;
+  } else if (plan->total_new > 0) {
     AppendParams ap = append_params(pr, args, plan->total_new, status);
     cudaError_t e = launch_kv_append(ap, pr.head_dim, pr.cache_dtype == PKV_FP8_E4M3, s);
     if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
@@ -333,11 +509,12 @@ extern "C" pkv_status pkv_attn_varlen_kvcache_fwd(const pkv_problem* problem, co
   // append kernel and the combine kernel's start with the attention's end.
   // Plans with prefill tiles keep the kernels strictly in order: there the
   // overlap measured slower (large appends, long attention kernels).  Never
-  // across a profiling event, which must see the kernels in order.
+  // across a profiling event, which must see the kernels in order, nor over a
+  // rotating append, whose queries the attention reads from its start.
   const bool overlap = plan->num_prefill_items == 0;
   e = launch_attention(p, tk, tv, tq, plan->num_ctas, pr.head_dim, pr.cache_dtype == PKV_FP8_E4M3,
                        plan->num_prefill_items > 0, plan->num_decode_items > 0,
-                       overlap && plan->total_new > 0 && !g_ev_start, s);
+                       overlap && plan->total_new > 0 && !rope && !g_ev_start, s);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   if (g_ev_stop && (e = record_profile_event(g_ev_stop, s)) != cudaSuccess) return cuda_fail(e, "profile event");
 
@@ -357,6 +534,22 @@ extern "C" pkv_status pkv_attn_varlen_kvcache_fwd(const pkv_problem* problem, co
     if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   }
   return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status pkv_attn_varlen_kvcache_fwd(const pkv_problem* problem, const pkv_fwd_args* args,
+                                                  pkv_plan_t plan, void* workspace, size_t workspace_bytes,
+                                                  void* stream) {
+  return run_call(problem, args, nullptr, plan, workspace, workspace_bytes, stream);
+}
+
+extern "C" pkv_status pkv_rope_attn_varlen_kvcache_fwd(const pkv_problem* problem, const pkv_fwd_args* args,
+                                                       const pkv_rope_append_args* rope, pkv_plan_t plan,
+                                                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (!rope) return fail(PKV_ERR_INVALID_ARG, "rope arguments are NULL");
+  return run_call(problem, args, rope, plan, workspace, workspace_bytes, stream);
 }
 
 extern "C" pkv_status pkv_set_profile_events(void* start_event, void* stop_event) {

@@ -32,6 +32,26 @@ struct AppendParams {
   int* status;
 };
 
+// Norm + rotation of query and key rows (pkv_rope_spec), alone or on the way
+// into the cache.
+struct RopeParams {
+  const float* cos_sin;
+  int32_t num_positions, rot_dim, interleaved;
+  float eps;
+  const __nv_bfloat16* q_weight;
+  const __nv_bfloat16* k_weight;
+  const __nv_bfloat16* q;  // total_q rows of hq heads
+  int64_t q_stride_tok, q_stride_head;
+  __nv_bfloat16* q_out;
+  int64_t qo_stride_tok, qo_stride_head;
+  int32_t total_q, hq;
+  const int32_t* cu_q;       // append form: [batch + 1]
+  const int32_t* positions;  // plain form: [total_q]
+  // the keys (and, append form, values); plain form: k_out and its strides in
+  // k_cache, c_stride_tok and c_stride_head
+  AppendParams a;
+};
+
 struct CombineParams {
   const CombineItem* items;
   const int32_t* q_offsets;  // nullable: query row offsets of the sequences (rows placed by the caller)
@@ -93,6 +113,8 @@ __device__ __forceinline__ const int32_t* seq_pages(const int32_t* bt, int32_t s
 }
 
 cudaError_t launch_kv_append(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_rope_kv_append(const RopeParams& p, int head_dim, bool fp8, cudaStream_t stream);
 // overlap_prev: launch with programmatic stream serialization, so that the
 // kernel's start overlaps the end of the kernel issued just before it on the
 // stream (the append kernel for the attention, the attention for the combine);

@@ -1,0 +1,251 @@
+// Per-head RMS norm and rotary position of query and key rows, alone
+// (pkv_qk_norm_rope) or on the way into the KV cache (pkv_rope_kv_append).
+//
+// One warp per (token, run of heads).  A head's D values sit in D / 8 lanes, 8
+// a lane, as two 4-value pieces placed so that both members of every rotated
+// pair are in the same lane: with pairs (i, i + rot/2) lane l holds
+// 4l .. 4l+3 and rot/2 + 4l .. rot/2 + 4l+3, else 8l .. 8l+7.  So the rotation
+// exchanges nothing between lanes, each lane needs 4 cosines and 4 sines (not
+// 8 of each), and the norm's sum of squares is one shuffle tree of D / 8 lanes.
+//
+// Everything is fp32 from the bf16 input to the one rounding at the end.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ void unpack4(uint2 v, float* f) {
+  f[0] = bf_lo(v.x);
+  f[1] = bf_hi(v.x);
+  f[2] = bf_lo(v.y);
+  f[3] = bf_hi(v.y);
+}
+
+__device__ __forceinline__ uint32_t codes4(const float* f, float inv) {
+  return (uint32_t)f32x2_to_e4m3x2(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
+         ((uint32_t)f32x2_to_e4m3x2(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv)) << 16);
+}
+
+// The largest b in [0, batch) with cu[b] <= t, found by the whole warp: each
+// step probes 32 boundaries at once (two dependent loads up to 1024 sequences).
+__device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = batch;
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const bool in = lane * step < n && __ldg(cu + lo + lane * step) <= t;
+    const int c = max(1, __popc(__ballot_sync(0xffffffffu, in))) - 1;
+    lo += c * step;
+    n = min(step, n - c * step);
+  }
+  return lo;
+}
+
+// One head's lane share: norm and rotation of the 8 values x (pieces 0..3, 4..7).
+// (the operations are spelled out, so that every instance gives the same bits:
+// a row rotated alone equals the row rotated into a bf16 cache)
+template <int D>
+__device__ __forceinline__ void transform(float* x, bool norm, const float* w, float eps, bool rot, bool pairs,
+                                          const float* cs, const float* sn) {
+  if (norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __fmaf_rn(x[i], x[i], ss);
+#pragma unroll
+    for (int o = D / 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(__fmaf_rn(ss, 1.f / D, eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+  }
+  if (rot) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int a = pairs ? 2 * i : i, b = pairs ? 2 * i + 1 : i + 4;
+      const float u = x[a], v = x[b];
+      x[a] = __fmaf_rn(u, cs[i], -__fmul_rn(v, sn[i]));
+      x[b] = __fmaf_rn(v, cs[i], __fmul_rn(u, sn[i]));
+    }
+  }
+}
+
+// APPEND: keys go into the cache (FP8: as e4m3 codes) with the values, positions
+// follow from cache_seqlens; else keys go to k_out and positions are given.
+// HC: heads of a warp's run, per D / 8 lanes.
+template <int D, bool APPEND, bool FP8, bool PAIRS, int HC>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kLanes = D / 8;          // lanes of a head
+  constexpr int kHeads = 32 / kLanes;    // heads side by side in a warp
+  constexpr int kRun = kHeads * HC;      // heads of a warp
+  grid_dep_launch();  // (attention calls order themselves behind this grid)
+  const int lane = threadIdx.x & 31;
+  const int l = lane % kLanes, sub = lane / kLanes;
+  const int uq = (p.hq + kRun - 1) / kRun, uk = (p.a.hkv + kRun - 1) / kRun;
+  const int units = uq + (APPEND ? 2 : 1) * uk;
+  const int64_t wi = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
+  const int64_t t64 = wi / units;
+  if (t64 >= max(p.total_q, p.a.total_new)) return;
+  const int t = (int)t64;
+  const int u = (int)(wi - t64 * units);
+  // what this warp does: 0 queries, 1 keys, 2 values (of the append)
+  const int part = u < uq ? 0 : (u < uq + uk ? 1 : 2);
+  if (t >= (part == 0 ? p.total_q : p.a.total_new)) return;
+  const int heads = part == 0 ? p.hq : p.a.hkv;
+  const int h0 = (part == 0 ? u : part == 1 ? u - uq : u - uq - uk) * kRun + sub;
+
+  // this lane's two pieces, and whether they are rotated
+  const int half = p.rot_dim >> 1;
+  const bool rot = part < 2 && 8 * l < p.rot_dim;
+  const int pa = (!PAIRS && rot) ? 4 * l : 8 * l;
+  const int pb = (!PAIRS && rot) ? half + 4 * l : 8 * l + 4;
+
+  // the rows, all loads in flight before anything depends on one
+  const __nv_bfloat16* src = part == 0 ? p.q + (int64_t)t * p.q_stride_tok
+                                       : (part == 1 ? p.a.k_new : p.a.v_new) + (int64_t)t * p.a.n_stride_tok;
+  const int64_t src_head = part == 0 ? p.q_stride_head : p.a.n_stride_head;
+  uint2 raw[HC][2];
+#pragma unroll
+  for (int i = 0; i < HC; ++i) {
+    const int h = h0 + i * kHeads;
+    raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+    if (h < heads) {
+      raw[i][0] = *reinterpret_cast<const uint2*>(src + h * src_head + pa);
+      raw[i][1] = *reinterpret_cast<const uint2*>(src + h * src_head + pb);
+    }
+  }
+  float w[8];
+  const __nv_bfloat16* wt = part == 0 ? p.q_weight : p.k_weight;
+  const bool norm = part < 2 && wt != nullptr;
+  if (norm) {
+    unpack4(__ldg(reinterpret_cast<const uint2*>(wt + pa)), w);
+    unpack4(__ldg(reinterpret_cast<const uint2*>(wt + pb)), w + 4);
+  }
+
+  // position, and (append) the cache row
+  int pos = 0, b = 0;
+  int64_t dst = 0;
+  if constexpr (APPEND) {
+    if (part == 0) {
+      b = find_seq(p.cu_q, p.a.batch, t);
+      const int q0 = __ldg(p.cu_q + b), lq = __ldg(p.cu_q + b + 1) - q0;
+      const int ln = p.a.total_new > 0 ? __ldg(p.a.cu_knew + b + 1) - __ldg(p.a.cu_knew + b) : 0;
+      pos = __ldg(p.a.cache_seqlens + b) + ln - lq + (t - q0);
+    } else {
+      b = find_seq(p.a.cu_knew, p.a.batch, t);
+      pos = __ldg(p.a.cache_seqlens + b) + (t - __ldg(p.a.cu_knew + b));
+      if (pos < 0 || pos >= p.a.capacity) {
+        if (lane == 0) record_status(p.a.status, PKV_ERR_DEVICE_BOUNDS, b, pos);
+        return;
+      }
+      if (p.a.page_size > 0) {
+        int npages;
+        const int32_t* pages = seq_pages(p.a.block_table, p.a.bt_stride, p.a.page_indptr, b, &npages);
+        const int pi = pos / p.a.page_size;
+        const int page = (npages >= 0 && pi >= npages) ? -1 : __ldg(pages + pi);
+        if (page < 0 || page >= p.a.num_pages) {
+          if (lane == 0) record_status(p.a.status, PKV_ERR_DEVICE_BOUNDS, b, page);
+          return;
+        }
+        dst = (int64_t)page * p.a.c_stride_page + (int64_t)(pos - pi * p.a.page_size) * p.a.c_stride_tok;
+      } else {
+        dst = (int64_t)b * p.a.c_stride_page + (int64_t)pos * p.a.c_stride_tok;
+      }
+    }
+  } else {
+    pos = p.rot_dim > 0 ? __ldg(p.positions + t) : 0;
+    b = t;
+  }
+  // (a value row is skipped with its key row)
+  if (p.rot_dim > 0 && (pos < 0 || pos >= p.num_positions)) {
+    if (lane == 0) record_status(p.a.status, PKV_ERR_DEVICE_BOUNDS, b, pos);
+    return;
+  }
+  float cs[4], sn[4];
+  if (rot) {
+    const float* row = p.cos_sin + (int64_t)pos * p.rot_dim + 4 * l;
+    const float4 c4 = __ldg(reinterpret_cast<const float4*>(row));
+    const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + half));
+    cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
+    sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
+  }
+
+  // (one IEEE reciprocal, as the plain append encodes)
+  const float inv = (FP8 && part > 0) ? __frcp_rn(__ldg(part == 1 ? p.a.k_scale : p.a.v_scale)) : 1.f;
+#pragma unroll
+  for (int i = 0; i < HC; ++i) {
+    const int h = h0 + i * kHeads;
+    float x[8];
+    unpack4(raw[i][0], x);
+    unpack4(raw[i][1], x + 4);
+    transform<D>(x, norm, w, p.eps, rot, PAIRS, cs, sn);  // (shuffles: every lane of the warp)
+    if (h >= heads) continue;
+    if (FP8 && part > 0) {
+      uint8_t* out = static_cast<uint8_t*>(part == 1 ? p.a.k_cache : p.a.v_cache) + dst + h * p.a.c_stride_head;
+      *reinterpret_cast<uint32_t*>(out + pa) = codes4(x, inv);
+      *reinterpret_cast<uint32_t*>(out + pb) = codes4(x + 4, inv);
+      continue;
+    }
+    __nv_bfloat16* out;
+    if (part == 0)
+      out = p.q_out + (int64_t)t * p.qo_stride_tok + h * p.qo_stride_head;
+    else if (APPEND)
+      out = static_cast<__nv_bfloat16*>(part == 1 ? p.a.k_cache : p.a.v_cache) + dst + h * p.a.c_stride_head;
+    else
+      out = static_cast<__nv_bfloat16*>(p.a.k_cache) + (int64_t)t * p.a.c_stride_tok + h * p.a.c_stride_head;
+    if (part == 2) {  // values: the bits as they came
+      *reinterpret_cast<uint2*>(out + pa) = raw[i][0];
+      *reinterpret_cast<uint2*>(out + pb) = raw[i][1];
+    } else {
+      *reinterpret_cast<uint2*>(out + pa) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      *reinterpret_cast<uint2*>(out + pb) = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    }
+  }
+}
+
+template <int D, bool APPEND, bool FP8, bool PAIRS, int HC>
+cudaError_t launch_run(const RopeParams& p, cudaStream_t stream) {
+  constexpr int kRun = (256 / D) * HC;
+  const int64_t uq = (p.hq + kRun - 1) / kRun, uk = (p.a.hkv + kRun - 1) / kRun;
+  const int64_t warps = (int64_t)std::max(p.total_q, p.a.total_new) * (uq + (APPEND ? 2 : 1) * uk);
+  const int64_t blocks = (warps * 32 + kRopeThreads - 1) / kRopeThreads;
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  rope_kernel<D, APPEND, FP8, PAIRS, HC><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, bool APPEND, bool FP8>
+cudaError_t launch_d(const RopeParams& p, cudaStream_t stream) {
+  return p.interleaved ? launch_run<D, APPEND, FP8, true, 1>(p, stream)
+                       : launch_run<D, APPEND, FP8, false, 1>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, cudaStream_t stream) {
+  return head_dim == 256   ? launch_d<256, false, false>(p, stream)
+         : head_dim == 128 ? launch_d<128, false, false>(p, stream)
+                           : launch_d<64, false, false>(p, stream);
+}
+
+cudaError_t launch_rope_kv_append(const RopeParams& p, int head_dim, bool fp8, cudaStream_t stream) {
+  if (fp8)
+    return head_dim == 256   ? launch_d<256, true, true>(p, stream)
+           : head_dim == 128 ? launch_d<128, true, true>(p, stream)
+                             : launch_d<64, true, true>(p, stream);
+  return head_dim == 256   ? launch_d<256, true, false>(p, stream)
+         : head_dim == 128 ? launch_d<128, true, false>(p, stream)
+                           : launch_d<64, true, false>(p, stream);
+}
+
+}  // namespace pkv
