@@ -1,7 +1,8 @@
 // Per-head RMS norm and rotary position of query and key rows, alone
 // (pkv_qk_norm_rope) or on the way into the KV cache (pkv_rope_kv_append).
 //
-// One warp per (token, run of heads).  A head's D values sit in D / 8 lanes, 8
+// One warp per (token, run of heads); a block's warps take consecutive tokens,
+// consecutive blocks the runs of the same tokens.  A head's D values sit in D / 8 lanes, 8
 // a lane, as two 4-value pieces placed so that both members of every rotated
 // pair are in the same lane: with pairs (i, i + rot/2) lane l holds
 // 4l .. 4l+3 and rot/2 + 4l .. rot/2 + 4l+3, else 8l .. 8l+7.  So the rotation
@@ -9,6 +10,12 @@
 // 8 of each), and the norm's sum of squares is one shuffle tree of D / 8 lanes.
 //
 // Everything is fp32 from the bf16 input to the one rounding at the end.
+//
+// Bound by HBM on large calls (131072 tokens, 32 + 8 heads of 128: norm + rotation
+// 480 us = 5.74 TB/s, 84% of the measured copy bandwidth; append to an fp8 cache
+// 449 us = 6.58 TB/s, 97%), by the launch and a chain of three dependent loads
+// (sequence, length, page or table row) on a decode batch (64 tokens: 1.9 us norm +
+// rotation, 2.8 us append).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -20,7 +27,8 @@ namespace pkv {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = 4;  // (8: 18.5 against 17.8 us on 4093 tokens, 469 against 449 on the 131072-token fp8 append)
+constexpr int kRopeThreads = 32 * kRopeWarps;
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -92,11 +100,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int l = lane % kLanes, sub = lane / kLanes;
   const int uq = (p.hq + kRun - 1) / kRun, uk = (p.a.hkv + kRun - 1) / kRun;
   const int units = uq + (APPEND ? 2 : 1) * uk;
-  const int64_t wi = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
-  const int64_t t64 = wi / units;
-  if (t64 >= max(p.total_q, p.a.total_new)) return;
-  const int t = (int)t64;
-  const int u = (int)(wi - t64 * units);
+  const int tb = blockIdx.x / units, u = blockIdx.x - tb * units;
+  const int t = tb * kRopeWarps + (threadIdx.x >> 5);
   // what this warp does: 0 queries, 1 keys, 2 values (of the append)
   const int part = u < uq ? 0 : (u < uq + uk ? 1 : 2);
   if (t >= (part == 0 ? p.total_q : p.a.total_new)) return;
@@ -116,11 +121,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   uint2 raw[HC][2];
 #pragma unroll
   for (int i = 0; i < HC; ++i) {
-    const int h = h0 + i * kHeads;
     raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
-    if (h < heads) {
-      raw[i][0] = *reinterpret_cast<const uint2*>(src + h * src_head + pa);
-      raw[i][1] = *reinterpret_cast<const uint2*>(src + h * src_head + pb);
+    if (h0 + i * kHeads < heads) {
+      raw[i][0] = *reinterpret_cast<const uint2*>(src + (h0 + i * kHeads) * src_head + pa);
+      raw[i][1] = *reinterpret_cast<const uint2*>(src + (h0 + i * kHeads) * src_head + pb);
     }
   }
   float w[8];
@@ -181,33 +185,34 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
   // (one IEEE reciprocal, as the plain append encodes)
   const float inv = (FP8 && part > 0) ? __frcp_rn(__ldg(part == 1 ? p.a.k_scale : p.a.v_scale)) : 1.f;
+  // where the rows go
+  uint8_t* out = static_cast<uint8_t*>(part == 2 ? p.a.v_cache : p.a.k_cache);
+  int64_t out_head = p.a.c_stride_head * (FP8 ? 1 : 2);
+  if constexpr (APPEND) out += dst * (FP8 ? 1 : 2);
+  else out += (int64_t)t * p.a.c_stride_tok * 2;
+  if (part == 0) {
+    out = reinterpret_cast<uint8_t*>(p.q_out + (int64_t)t * p.qo_stride_tok);
+    out_head = p.qo_stride_head * 2;
+  }
 #pragma unroll
   for (int i = 0; i < HC; ++i) {
     const int h = h0 + i * kHeads;
+    if (h - sub >= heads) break;  // (warp-uniform)
     float x[8];
     unpack4(raw[i][0], x);
     unpack4(raw[i][1], x + 4);
     transform<D>(x, norm, w, p.eps, rot, PAIRS, cs, sn);  // (shuffles: every lane of the warp)
-    if (h >= heads) continue;
+    if (h >= heads) break;
+    uint8_t* row = out + h * out_head;
     if (FP8 && part > 0) {
-      uint8_t* out = static_cast<uint8_t*>(part == 1 ? p.a.k_cache : p.a.v_cache) + dst + h * p.a.c_stride_head;
-      *reinterpret_cast<uint32_t*>(out + pa) = codes4(x, inv);
-      *reinterpret_cast<uint32_t*>(out + pb) = codes4(x + 4, inv);
-      continue;
-    }
-    __nv_bfloat16* out;
-    if (part == 0)
-      out = p.q_out + (int64_t)t * p.qo_stride_tok + h * p.qo_stride_head;
-    else if (APPEND)
-      out = static_cast<__nv_bfloat16*>(part == 1 ? p.a.k_cache : p.a.v_cache) + dst + h * p.a.c_stride_head;
-    else
-      out = static_cast<__nv_bfloat16*>(p.a.k_cache) + (int64_t)t * p.a.c_stride_tok + h * p.a.c_stride_head;
-    if (part == 2) {  // values: the bits as they came
-      *reinterpret_cast<uint2*>(out + pa) = raw[i][0];
-      *reinterpret_cast<uint2*>(out + pb) = raw[i][1];
+      *reinterpret_cast<uint32_t*>(row + pa) = codes4(x, inv);
+      *reinterpret_cast<uint32_t*>(row + pb) = codes4(x + 4, inv);
+    } else if (part == 2) {  // values: the bits as they came
+      *reinterpret_cast<uint2*>(row + 2 * pa) = raw[i][0];
+      *reinterpret_cast<uint2*>(row + 2 * pb) = raw[i][1];
     } else {
-      *reinterpret_cast<uint2*>(out + pa) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-      *reinterpret_cast<uint2*>(out + pb) = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+      *reinterpret_cast<uint2*>(row + 2 * pa) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      *reinterpret_cast<uint2*>(row + 2 * pb) = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
     }
   }
 }
@@ -216,18 +221,35 @@ template <int D, bool APPEND, bool FP8, bool PAIRS, int HC>
 cudaError_t launch_run(const RopeParams& p, cudaStream_t stream) {
   constexpr int kRun = (256 / D) * HC;
   const int64_t uq = (p.hq + kRun - 1) / kRun, uk = (p.a.hkv + kRun - 1) / kRun;
-  const int64_t warps = (int64_t)std::max(p.total_q, p.a.total_new) * (uq + (APPEND ? 2 : 1) * uk);
-  const int64_t blocks = (warps * 32 + kRopeThreads - 1) / kRopeThreads;
+  const int64_t tokens = std::max(p.total_q, p.a.total_new);
+  const int64_t blocks = (tokens + kRopeWarps - 1) / kRopeWarps * (uq + (APPEND ? 2 : 1) * uk);
   if (blocks == 0) return cudaSuccess;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   rope_kernel<D, APPEND, FP8, PAIRS, HC><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
+template <int D, bool APPEND, bool FP8, int HC>
+cudaError_t launch_hc(const RopeParams& p, cudaStream_t stream) {
+  return p.interleaved ? launch_run<D, APPEND, FP8, true, HC>(p, stream)
+                       : launch_run<D, APPEND, FP8, false, HC>(p, stream);
+}
+
+// Heads a lane takes one after another (their loads all in flight at once): 1
+// while every warp of that split runs at once (152 SMs x 40), where a call is
+// latency; 4 from twice that on, where a warp's lookups (sequence, position,
+// table row, weights) are worth spreading over more rows; 2 between.  Measured
+// at 32 + 8 heads of 128 (a call inside a captured graph): norm + rotation of 64
+// tokens 1.85 / 1.93 / 2.29 us at 1 / 2 / 4, of 512 5.30 / 4.29 / 4.67, of 4096
+// 26.9 / 20.0 / 18.0; append of 64 tokens 2.79 / 2.75 / 2.95, of 4096 34.7 /
+// 21.7 / 17.7.  8 was slower than 4 on every size but one.
 template <int D, bool APPEND, bool FP8>
 cudaError_t launch_d(const RopeParams& p, cudaStream_t stream) {
-  return p.interleaved ? launch_run<D, APPEND, FP8, true, 1>(p, stream)
-                       : launch_run<D, APPEND, FP8, false, 1>(p, stream);
+  constexpr int kHeads = 256 / D;
+  const int64_t warps = (int64_t)std::max(p.total_q, p.a.total_new) *
+                        ((p.hq + kHeads - 1) / kHeads + (APPEND ? 2 : 1) * ((p.a.hkv + kHeads - 1) / kHeads));
+  if (warps <= 6080) return launch_hc<D, APPEND, FP8, 1>(p, stream);
+  return warps < 12160 ? launch_hc<D, APPEND, FP8, 2>(p, stream) : launch_hc<D, APPEND, FP8, 4>(p, stream);
 }
 
 }  // namespace

@@ -280,6 +280,25 @@ def test_qk_norm_rope(pkv, gpu, d, rot, interleaved, norm, tokens, hq, hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [401, 701])       # two, four heads a lane
+@pytest.mark.parametrize("d,hq,hkv,interleaved", [(64, 66, 19, False), (128, 33, 9, True), (256, 17, 5, False)])
+def test_many_rows(pkv, gpu, tokens, d, hq, hkv, interleaved):
+    """The splits of heads that larger calls take, at head counts that do not fill them; alone and into the cache."""
+    torch = gpu
+    c = AppendCase(pkv, torch, tokens + d, d=d, page=16, fp8=d == 128, new=[tokens - 150, 0, 150], cached=[0, 3, 37],
+                   hq=hq, hkv=hkv, rot=d // 2, interleaved=interleaved, norm="qk")
+    k0, v0 = H.to_numpy_bits(c.kc).copy(), H.to_numpy_bits(c.vc).copy()
+    c.run()
+    assert int(c.status[0]) == 0
+    c.check(k0, v0)
+    pq, _, _ = c.positions()
+    q, k, positions = torch.empty_like(c.q_out), torch.empty(c.k.shape, dtype=c.k.dtype, device="cuda"), H.i32(pq)
+    pkv.qk_norm_rope(pkv.make_qk_args(q=c.q, k=c.k, positions=positions, q_out=q, k_out=k), c.spec)
+    assert torch.equal(q, c.q_out)
+    close_bf16(k, *rows64(np64(c.k), np64(c.kw), pq, c.table, interleaved, c.eps))
+
+
+@pytest.mark.gpu
 def test_qk_norm_rope_one_side_and_strides(pkv, gpu):
     """q alone, k alone, heads outermost, another stream."""
     torch = gpu
