@@ -200,6 +200,40 @@ pkv_status pkv_plan_decode_dynamic(const pkv_problem* problem, const int32_t* h_
                                    const int32_t* h_max_cache_lens, const int32_t* h_new_lens,
                                    int32_t num_sms, pkv_plan_t* out_plan, size_t* out_workspace_bytes);
 
+/*
+ * pkv_plan_shared_prefix -- a plan for a batch whose sequences share long
+ * prefixes (one system prompt under many requests, several samples of one
+ * prompt, a prefix cache's common pages): the keys of a shared prefix are
+ * attended once for all the queries of its group, in common tiles, and merged
+ * with each sequence's own keys by their log-sum-exp,
+ *   lse = log sum_s exp(lse_s),  out = sum_s exp(lse_s - lse) out_s.
+ * The plan is uploaded and run like any other (pkv_attn_varlen_kvcache_fwd and
+ * its rotating and workspace-free forms) and gives what pkv_plan's would, up to
+ * rounding.
+ * Group g is the sequences h_group_starts[g] .. h_group_starts[g+1] - 1
+ * ([num_groups + 1], rising, at most batch; sequences outside every group, or
+ * in one with prefix 0, share nothing).  The first h_prefix_lens[g] tokens of
+ * each of them lie in the same pages: their block tables (or page lists) start
+ * with the same page numbers.  The library reads the shared keys through the
+ * group's first sequence with queries; it shares whole pages (prefix_len rounded down
+ * to page_size).  h_cache_lens[b] >= prefix_len for every sequence of the group,
+ * so nothing is appended into a shared page.  Sequences whose queries do not
+ * fit one tile (as for pkv_plan_decode_dynamic), or (causal) do not all see the
+ * whole prefix, are planned as without it, and so is a group whose common tiles
+ * (16 rows, else 128 / (Hq/Hkv) query tokens each) would be no fewer than its
+ * sequences.
+ * dynamic = 0: lengths as in pkv_plan; 1: as in pkv_plan_decode_dynamic
+ * (h_cache_lens are bounds, the prefixes are fixed; a call whose
+ * cache_seqlens[b] is below its prefix records PKV_ERR_PLAN_MISMATCH).
+ * A contiguous cache (page_size 0) stores a copy of the prefix per sequence:
+ * PKV_ERR_UNSUPPORTED, and so is a call with q_rows > 0.  Pure host code.
+ */
+pkv_status pkv_plan_shared_prefix(const pkv_problem* problem, const int32_t* h_q_lens,
+                                  const int32_t* h_cache_lens, const int32_t* h_new_lens,
+                                  int32_t num_groups, const int32_t* h_group_starts,
+                                  const int32_t* h_prefix_lens, int32_t dynamic, int32_t num_sms,
+                                  pkv_plan_t* out_plan, size_t* out_workspace_bytes);
+
 /* Copies the plan's work list into the caller's device workspace on `stream`
  * (asynchronously; the host copy stays valid until pkv_plan_destroy) and clears
  * the device status word.  Must precede pkv_attn_varlen_kvcache_fwd with this
@@ -210,7 +244,9 @@ pkv_status pkv_plan_upload(pkv_plan_t plan, void* workspace, size_t workspace_by
 /* Statistics of a plan (host only). */
 pkv_status pkv_plan_get_stats(pkv_plan_t plan, pkv_plan_stats* stats);
 
-/* One scheduled tile as the plan made it (diagnostics and tests).  Rows of a
+/* One scheduled tile as the plan made it (diagnostics and tests).  A tile over a
+ * shared prefix has seq = the first of its sequences, q_row0 .. q_row0 + n_q - 1
+ * rows of several of them, q_len = 1 and kv_len = the shared keys.  Rows of a
  * tile are (query token, head of the tile's heads) pairs, row = token *
  * num_heads + g, query head = kv_head * G + head0 + g. */
 typedef struct {

@@ -27,7 +27,8 @@ STATUS_NAMES = {
 EXPORTED = ["pkv_plan", "pkv_plan_upload", "pkv_plan_get_stats", "pkv_plan_get_items", "pkv_attn_varlen_kvcache_fwd", "pkv_kv_append",
             "pkv_get_status", "pkv_plan_destroy", "pkv_last_error", "pkv_version", "pkv_set_profile_events",
             "pkv_attn_varlen_kvcache_fwd_noalloc", "pkv_plan_decode_dynamic", "pkv_get_status_noalloc",
-            "pkv_qk_norm_rope", "pkv_rope_kv_append", "pkv_rope_attn_varlen_kvcache_fwd"]
+            "pkv_qk_norm_rope", "pkv_rope_kv_append", "pkv_rope_attn_varlen_kvcache_fwd",
+            "pkv_plan_shared_prefix"]
 
 
 class PkvError(RuntimeError):
@@ -103,6 +104,8 @@ def lib() -> ctypes.CDLL:
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         L.pkv_plan.argtypes = [ctypes.POINTER(Problem), vp, vp, vp, i32, ctypes.POINTER(vp), ctypes.POINTER(sz)]
         L.pkv_plan_decode_dynamic.argtypes = L.pkv_plan.argtypes
+        L.pkv_plan_shared_prefix.argtypes = [ctypes.POINTER(Problem), vp, vp, vp, i32, vp, vp, i32, i32,
+                                             ctypes.POINTER(vp), ctypes.POINTER(sz)]
         L.pkv_plan_upload.argtypes = [vp, vp, sz, vp]
         L.pkv_plan_get_stats.argtypes = [vp, ctypes.POINTER(PlanStats)]
         L.pkv_plan_get_items.argtypes = [vp, ctypes.POINTER(WorkItemInfo), i32, ctypes.POINTER(i32)]
@@ -264,17 +267,29 @@ def make_rope_append_args(*, spec: RopeSpec, q_out=None) -> RopeAppendArgs:
 class Plan:
     """Host work list made by ``pkv_plan`` (owned until ``close``)."""
 
-    def __init__(self, problem: Problem, q_lens, cache_lens, new_lens, num_sms: int, dynamic: bool = False):
+    def __init__(self, problem: Problem, q_lens, cache_lens, new_lens, num_sms: int, dynamic: bool = False,
+                 shared=None):
         import numpy as np
+        for what, lens in (("q_lens", q_lens), ("cache_lens", cache_lens), ("new_lens", new_lens)):
+            if shared is not None and lens is not None and len(lens) != problem.batch:
+                raise ValueError(f"{what}: {problem.batch} sequences expected, got {len(lens)}")
         self.problem = problem
         self._q = np.ascontiguousarray(q_lens, dtype=np.int32)
         self._c = np.ascontiguousarray(cache_lens, dtype=np.int32)
         self._n = None if new_lens is None else np.ascontiguousarray(new_lens, dtype=np.int32)
         h = ctypes.c_void_p()
         ws = ctypes.c_size_t()
-        fn = lib().pkv_plan_decode_dynamic if dynamic else lib().pkv_plan
-        _check(fn(ctypes.byref(problem), self._q.ctypes.data, self._c.ctypes.data,
-                  None if self._n is None else self._n.ctypes.data, int(num_sms), ctypes.byref(h), ctypes.byref(ws)))
+        lens = (ctypes.byref(problem), self._q.ctypes.data, self._c.ctypes.data,
+                None if self._n is None else self._n.ctypes.data)
+        if shared is not None:  # (group_starts, prefix_lens)
+            starts, prefixes = (np.ascontiguousarray(x, dtype=np.int32) for x in shared)
+            if len(starts) != len(prefixes) + 1:
+                raise ValueError(f"{len(prefixes)} prefix_lens need {len(prefixes) + 1} group_starts, got {len(starts)}")
+            _check(lib().pkv_plan_shared_prefix(*lens, len(prefixes), starts.ctypes.data, prefixes.ctypes.data,
+                                                int(dynamic), int(num_sms), ctypes.byref(h), ctypes.byref(ws)))
+        else:
+            fn = lib().pkv_plan_decode_dynamic if dynamic else lib().pkv_plan
+            _check(fn(*lens, int(num_sms), ctypes.byref(h), ctypes.byref(ws)))
         self.handle = h
         self.workspace_bytes = int(ws.value)
 
@@ -321,6 +336,18 @@ def plan_decode_dynamic(problem: Problem, q_lens, max_cache_lens, new_lens=None,
         import torch
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
     return Plan(problem, q_lens, max_cache_lens, new_lens, num_sms, dynamic=True)
+
+
+def plan_shared_prefix(problem: Problem, q_lens, cache_lens, new_lens=None, *, group_starts, prefix_lens,
+                       dynamic: bool = False, num_sms: Optional[int] = None) -> Plan:
+    """A plan for groups of consecutive sequences (group g: group_starts[g] ..
+    group_starts[g+1] - 1) whose first prefix_lens[g] tokens lie in the same
+    pages: the prefix is attended once for the whole group.  dynamic: as
+    ``plan_decode_dynamic`` (cache_lens are bounds)."""
+    if num_sms is None:
+        import torch
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return Plan(problem, q_lens, cache_lens, new_lens, num_sms, dynamic=dynamic, shared=(group_starts, prefix_lens))
 
 
 def attn_varlen_kvcache_fwd(problem: Problem, args: FwdArgs, plan_: Plan, workspace, stream=None) -> None:

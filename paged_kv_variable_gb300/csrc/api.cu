@@ -397,6 +397,8 @@ pkv_status validate_call(const pkv_problem* problem, const pkv_fwd_args* args, p
       return fail(PKV_ERR_INVALID_ARG, "q_rows %d < the plan's %d query rows", args->q_rows, plan->total_q);
   }
   if (args->q_rows < 0) return fail(PKV_ERR_INVALID_ARG, "q_rows < 0");
+  if (args->q_rows > 0 && plan->shared)
+    return fail(PKV_ERR_UNSUPPORTED, "a plan with shared prefixes takes packed query rows (q_rows = 0)");
   const bool has_new = args->k_new != nullptr || args->v_new != nullptr;
   if (plan->total_new > 0 && !has_new)
     return fail(PKV_ERR_INVALID_ARG, "the plan appends %d tokens but k_new / v_new are NULL", plan->total_new);
@@ -495,6 +497,7 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
   p.status = status;
   p.cache_seqlens = args->cache_seqlens;
   p.plan_lc = reinterpret_cast<const int32_t*>(ws + plan->layout.plan_lc);
+  p.plan_min = plan->shared && plan->dynamic ? reinterpret_cast<const int32_t*>(ws + plan->layout.plan_min) : nullptr;
   p.batch = pr.batch;
   p.dynamic = plan->dynamic;
   p.row_gather = pr.page_size > 0 && pr.page_size < kBoxRows;
@@ -530,7 +533,8 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
     cp.lse = p.lse;
     cp.total_q = p.total_q;
     cp.G = p.G;
-    e = launch_combine(cp, plan->num_combine, pr.head_dim, overlap && !g_ev_stop, s);
+    e = plan->shared ? launch_combine_shared(cp, plan->num_combine, pr.head_dim, overlap && !g_ev_stop, s)
+                     : launch_combine(cp, plan->num_combine, pr.head_dim, overlap && !g_ev_stop, s);
     if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   }
   return PKV_OK;

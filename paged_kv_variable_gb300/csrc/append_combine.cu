@@ -147,6 +147,88 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
   }
 }
 
+// The merge for plans with shared prefixes: a unit's rows have parts over the
+// chunks of the prefix, in the tiles of the sequences that share it, and parts
+// over the sequence's own keys.  One warp per row: each lane takes the LSE of
+// one part (the common max and the weights come from the warp's lanes), then
+// D / 32 columns of every part's row.  Parts are added in a fixed order, the
+// prefix's first.
+constexpr int kSharedCombineThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kSharedCombineThreads) combine_shared_kernel(const CombineParams p) {
+  constexpr int E = D / 32;  // columns of a lane: 8, 4 or 2
+  constexpr float kLn2 = 0.693147180559945309f;
+  const CombineItem ci = p.items[blockIdx.x];
+  const int lane = threadIdx.x & 31;
+  const int rows = ci.n_q * ci.nh, parts = ci.p_nsplit + ci.nsplit;
+  grid_dep_wait();  // the partials come from the attention kernel launched just before
+  for (int row = threadIdx.x >> 5; row < rows; row += kSharedCombineThreads / 32) {
+    // partial row of part 0 of each kind, and the rows between its parts
+    const int tok = row / ci.nh, g = row - tok * ci.nh;
+    const int pt = ci.p_tok0 + tok;
+    const int64_t prow =
+        ci.p_nsplit == 0 ? 0
+                         : ((int64_t)ci.p_slot0 + (int64_t)(pt / ci.p_tq) * ci.p_tile_slots) * kDecodeRows +
+                               (pt % ci.p_tq) * ci.nh + g;
+    const int64_t orow = (int64_t)ci.slot0 * kDecodeRows + row;
+    auto part_row = [&](int s) {
+      return s < ci.p_nsplit ? prow + (int64_t)s * ci.p_chunk_slots * kDecodeRows
+                             : orow + (int64_t)(s - ci.p_nsplit) * ci.slot_stride * kDecodeRows;
+    };
+    float m = -INFINITY;
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.partial_lse[part_row(s)]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float mu = m == -INFINITY ? 0.f : m;
+    float wsum = 0.f;
+    float acc[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = 0.f;
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+      const int n = min(32, parts - s0);
+      const float w = lane < n ? ex2(p.partial_lse[part_row(s0 + lane)] - mu) : 0.f;
+      wsum += w;
+#pragma unroll 4
+      for (int s = 0; s < n; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        const float* src = p.partial_o + part_row(s0 + s) * D + lane * E;
+        if constexpr (E == 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          acc[0] = fmaf(ws, v.x, acc[0]);
+          acc[1] = fmaf(ws, v.y, acc[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src + i);
+            acc[i] = fmaf(ws, v.x, acc[i]);
+            acc[i + 1] = fmaf(ws, v.y, acc[i + 1]);
+            acc[i + 2] = fmaf(ws, v.z, acc[i + 2]);
+            acc[i + 3] = fmaf(ws, v.w, acc[i + 3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const int out_row = ci.q_row0 + tok, head = ci.hk * p.G + ci.h0 + g;
+    __nv_bfloat16* dst = p.out + (int64_t)out_row * p.o_stride_tok + (int64_t)head * p.o_stride_head + lane * E;
+    if constexpr (E == 2) {
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+    } else if constexpr (E == 4) {
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    } else {
+      *reinterpret_cast<uint4*>(dst) =
+          make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
+                     pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
+    }
+    if (p.lse != nullptr && lane == 0)
+      p.lse[(int64_t)head * p.total_q + out_row] = wsum > 0.f ? (mu + __log2f(wsum)) * kLn2 : -INFINITY;
+  }
+}
+
 cudaError_t launch_kv_append(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.total_new * p.hkv;
   if (rows == 0) return cudaSuccess;
@@ -185,6 +267,24 @@ cudaError_t launch_combine(const CombineParams& p, int num_items, int head_dim, 
   return head_dim == 256   ? cudaLaunchKernelEx(&cfg, combine_kernel<256>, p)
          : head_dim == 128 ? cudaLaunchKernelEx(&cfg, combine_kernel<128>, p)
                            : cudaLaunchKernelEx(&cfg, combine_kernel<64>, p);
+}
+
+cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int head_dim, bool overlap_prev,
+                                  cudaStream_t stream) {
+  if (num_items == 0) return cudaSuccess;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)num_items);
+  cfg.blockDim = dim3((unsigned)kSharedCombineThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap_prev ? 1 : 0;
+  return head_dim == 256   ? cudaLaunchKernelEx(&cfg, combine_shared_kernel<256>, p)
+         : head_dim == 128 ? cudaLaunchKernelEx(&cfg, combine_shared_kernel<128>, p)
+                           : cudaLaunchKernelEx(&cfg, combine_shared_kernel<64>, p);
 }
 
 }  // namespace pkv

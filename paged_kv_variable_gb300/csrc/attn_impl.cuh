@@ -222,7 +222,7 @@ __device__ __forceinline__ WorkItem load_item(const AttnParams& p, int it) {
   // rows placed by the caller: the sequence's query rows start where
   // cu_seqlens_q says (packed rows keep the plan's prefix sums, no load)
   if (p.q_offsets != nullptr) w.q_row0 = __ldg(p.q_offsets + w.b) + w.q_i0;
-  if (p.dynamic) {
+  if (p.dynamic && !w.prefix) {  // (a shared prefix keeps its length)
     const int bound = __ldg(p.plan_lc + w.b);
     const int lc = min(max(__ldg(p.cache_seqlens + w.b), 0), bound);
     w.lk = w.lk - bound + lc;  // the plan's key count holds bound + new tokens
@@ -1903,7 +1903,9 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
   if (blockIdx.x == 0 && mma_consumer) {
     for (int b = ctid; b < p.batch; b += 32 * L::kDecWarps) {
       const int lc = __ldg(p.cache_seqlens + b), planned = __ldg(p.plan_lc + b);
-      if (p.dynamic ? (lc < 0 || lc > planned) : lc != planned) record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
+      const int least = p.plan_min != nullptr ? __ldg(p.plan_min + b) : 0;
+      if (p.dynamic ? (lc < least || lc > planned) : lc != planned)
+        record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
     }
   }
   const float kscale = FP8 ? __ldg(p.k_scale) : 1.f;

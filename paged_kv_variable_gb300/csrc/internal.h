@@ -69,7 +69,9 @@ struct WorkItem {
   int32_t partial;   // -1: write the final output; else the first partial slot (16 rows each)
   int32_t h0;        // first query head of the group in this tile
   int32_t nh;        // heads of the group in this tile (rows = n_q * nh)
-  int32_t pad[3];
+  int32_t prefix;    // 1: keys of a shared prefix (b: the first of its sequences; lk: its key count,
+                     // whatever the current lengths); the rows may belong to several sequences
+  int32_t pad[2];
 };
 static_assert(sizeof(WorkItem) == 64, "WorkItem layout");
 
@@ -85,9 +87,13 @@ struct CombineItem {
   int32_t slot_stride;  // 16-row slots per chunk: ceil(n_q * nh / 16)
   int32_t h0;
   int32_t nh;
-  int32_t pad[3];
+  // parts over a shared prefix: p_nsplit chunks (0: none), p_chunk_slots slots
+  // apart from p_slot0, each of tiles of p_tile_slots slots holding p_tq tokens;
+  // this unit's first token is token p_tok0 of the sequences sharing the prefix
+  int32_t p_nsplit, p_slot0, p_chunk_slots, p_tq, p_tile_slots, p_tok0;
+  int32_t pad;
 };
-static_assert(sizeof(CombineItem) == 48, "CombineItem layout");
+static_assert(sizeof(CombineItem) == 64, "CombineItem layout");
 
 // Byte offsets of the sections of the caller's workspace.
 struct WorkspaceLayout {
@@ -96,6 +102,7 @@ struct WorkspaceLayout {
   size_t cta_begin;     // int32[num_ctas + 1]
   size_t combine;       // CombineItem[num_combine]
   size_t plan_lc;       // int32[B] cache lengths the plan was made for
+  size_t plan_min;      // int32[B] (shared-prefix plans) least cache lengths: the prefixes
   size_t partial_o;     // float[num_slots * kDecodeRows * D]
   size_t partial_lse;   // float[num_slots * kDecodeRows] (log2 domain)
   size_t total;
@@ -120,6 +127,7 @@ struct pkv_plan_s {
   int32_t num_items;
   int32_t num_combine;
   int32_t dynamic;  // cache lengths read on the device; plan_lc holds their bounds
+  int32_t shared;   // some prefix is computed once for several sequences
   double* item_cost;  // [num_items] model cost of each item, in work-list order
 };
 

@@ -14,6 +14,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <functional>
 #include <new>
 #include <vector>
@@ -29,6 +30,27 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 struct Tile {
   WorkItem item;
   double cost;
+};
+
+// Groups of consecutive sequences whose first prefix_lens[g] tokens are the same.
+struct SharedPrefixes {
+  int32_t num_groups;
+  const int32_t* starts;  // [num_groups + 1]
+  const int32_t* prefix_lens;
+};
+
+// Consecutive sequences whose queries attend the same `keys` first keys in
+// common tiles.
+struct PrefixRun {
+  int b0;         // first sequence (its pages are the ones read)
+  int tokens;     // query tokens of all its sequences
+  int64_t q_row;  // the first one's packed row
+  int keys;       // shared keys, a whole number of pages
+  bool dec;       // all rows in one warp-MMA tile
+  int tq, tiles;  // query tokens a tile, tiles
+  int nchunks, chunk;
+  int tile_slots;             // partial slots of a tile
+  std::vector<int32_t> slot0;  // first partial slot of each kv head
 };
 
 // Per-key model costs (relative units): a decode key streams 2*D*esize bytes
@@ -77,8 +99,8 @@ using namespace pkv;
 namespace {
 
 pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const int32_t* h_cache_lens,
-                     const int32_t* h_new_lens, int32_t num_sms, bool dynamic, pkv_plan_t* out_plan,
-                     size_t* out_workspace_bytes) {
+                     const int32_t* h_new_lens, int32_t num_sms, bool dynamic, const SharedPrefixes* groups,
+                     pkv_plan_t* out_plan, size_t* out_workspace_bytes) {
   if (!out_plan || !out_workspace_bytes) return fail(PKV_ERR_INVALID_ARG, "output pointers are NULL");
   *out_plan = nullptr;
   *out_workspace_bytes = 0;
@@ -112,6 +134,72 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
     any_decode |= h_q_lens[b] > 0 && is_decode(h_q_lens[b]);
     any_prefill |= h_q_lens[b] > 0 && !is_decode(h_q_lens[b]);
   }
+
+  // Shared prefixes: shared[b] keys of sequence b are attended by its run's
+  // common tiles, the rest by its own.  A prefix is shared in whole pages (the
+  // tokens of its last, partly filled page are each sequence's own).
+  std::vector<int32_t> shared(B, 0), least(B, 0), run_of(B, -1), run_tok(B, 0);
+  std::vector<PrefixRun> runs;
+  if (groups != nullptr) {
+    if (groups->num_groups < 0 || (groups->num_groups > 0 && (!groups->starts || !groups->prefix_lens)))
+      return fail(PKV_ERR_INVALID_ARG, "group arrays are NULL or their count is negative");
+    const int ng = groups->num_groups;
+    for (int g = 0; g < ng; ++g) {
+      const int b0 = groups->starts[g], b1 = groups->starts[g + 1], len = groups->prefix_lens[g];
+      if (b0 < 0 || b1 < b0 || b1 > B || (g > 0 && b0 < groups->starts[g - 1]))
+        return fail(PKV_ERR_INVALID_ARG, "group_starts must rise from 0 to at most the batch (group %d)", g);
+      if (len < 0) return fail(PKV_ERR_INVALID_ARG, "negative prefix length of group %d", g);
+      if (len == 0) continue;
+      if (p.page_size == 0)
+        return fail(PKV_ERR_UNSUPPORTED, "shared prefixes need a paged cache (a contiguous one stores a copy a sequence)");
+      const int keys = len / p.page_size * p.page_size;
+      PrefixRun run{};
+      int members = 0;
+      // A run is kept if its common tiles are fewer than its sequences, each
+      // of which would read the prefix for itself (never with head groups of
+      // more than 64, whose tiles hold one token).
+      auto close_run = [&]() {
+        run.dec = is_decode(run.tokens);
+        run.tq = run.dec ? run.tokens : tq_prefill;
+        run.tiles = run.tokens > 0 ? (run.tokens + run.tq - 1) / run.tq : 0;
+        if (run.tiles < members && keys > 0) {
+          run.keys = keys;
+          run.tile_slots = run.dec ? 1 : kPrefillRowsTc / kDecodeRows;
+          any_decode |= run.dec;
+          any_prefill |= !run.dec;
+          for (int b = run.b0, n = members; n > 0; ++b) {
+            if (h_q_lens[b] == 0) continue;
+            shared[b] = keys;
+            run_of[b] = (int)runs.size();
+            --n;
+          }
+          runs.push_back(run);
+        }
+        members = 0;
+        run = PrefixRun{};
+      };
+      for (int b = b0; b < b1; ++b) {
+        const int lq = h_q_lens[b], lc = h_cache_lens[b], ln = h_new_lens ? h_new_lens[b] : 0;
+        if (lq < 0 || lc < 0 || ln < 0) return fail(PKV_ERR_INVALID_ARG, "negative length at sequence %d", b);
+        if (lc < len)
+          return fail(PKV_ERR_INVALID_ARG, "sequence %d: cache length %d < the prefix of its group (%d)", b, lc, len);
+        least[b] = len;
+        if (lq == 0) continue;
+        // every query must see the whole prefix (causal: the first one does),
+        // and the queries fit one tile (long runs fill tiles of their own)
+        const int64_t lk = (int64_t)(dynamic ? len : lc) + ln;
+        if (!splittable(lq) || (p.causal && lk - lq + 1 < keys)) {
+          close_run();
+          continue;
+        }
+        if (members == 0) run.b0 = b;
+        run_tok[b] = run.tokens;
+        run.tokens += lq;
+        ++members;
+      }
+      close_run();
+    }
+  }
   const int tq_item = tq_prefill * (any_decode ? 1 : prefill_q_tiles(D, p.cache_dtype == PKV_FP8_E4M3));
   // decode-only plans over an fp8 cache at head dims up to 128, or a bf16 one
   // at head dim 64 (rows of 128 bytes), run two CTAs an SM
@@ -132,8 +220,10 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
                   "dynamic plans take requests whose queries fit one tile (sequence %d: %d query tokens > %d)", b, lq,
                   std::max(tq_prefill, dec_rows / G));
     if (lq > 0 && splittable(lq))
-      total_split_keys += (int64_t)(lc + ln) * p.num_heads_kv * (is_decode(lq) ? 1 : n_sub);
+      total_split_keys += (int64_t)(lc + ln - shared[b]) * p.num_heads_kv * (is_decode(lq) ? 1 : n_sub);
   }
+  for (const PrefixRun& r : runs)
+    total_split_keys += (int64_t)r.keys * r.tiles * p.num_heads_kv;
   if (total_q > INT32_MAX / 2 || total_new > INT32_MAX / 2)
     return fail(PKV_ERR_UNSUPPORTED, "total tokens too large");
 
@@ -155,7 +245,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   // and no combine kernel (the bf16 decode batch: 98.1 against 100.3 us a
   // call, the same attention kernel).  Judged on the model costs of a
   // longest-first placement; batches with a few long sequences stay split.
-  if (!any_prefill && total_split_keys > 0) {
+  if (!any_prefill && runs.empty() && total_split_keys > 0) {
     const int ctas = num_sms * cps;
     std::vector<double> c, load;
     c.reserve((size_t)B * 4);
@@ -184,6 +274,11 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   }
   auto nchunks_of = [&](int lk) { return lk <= chunk ? 1 : (int)((lk + chunk - 1) / chunk); };
 
+  for (PrefixRun& r : runs) {
+    r.chunk = (int)std::min<int64_t>(chunk, r.keys);
+    r.nchunks = (r.keys + r.chunk - 1) / r.chunk;
+  }
+
   int64_t num_tiles_est = 0;
   for (int b = 0; b < B; ++b) {
     const int lq = h_q_lens[b], lk = h_cache_lens[b] + (h_new_lens ? h_new_lens[b] : 0);
@@ -198,6 +293,43 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   int64_t num_slots = 0;
   int32_t n_dec = 0, n_pre = 0;
   int64_t q_row = 0;
+  for (int b = 0, r = 0; b < B; ++b) {
+    if (r < (int)runs.size() && runs[r].b0 == b) runs[r++].q_row = q_row;
+    q_row += h_q_lens[b];
+  }
+  // the tiles over the shared prefixes: every tile of a run's query tokens
+  // against every chunk of the prefix, each into its own partial slots
+  for (PrefixRun& r : runs) {
+    for (int hk = 0; hk < p.num_heads_kv; ++hk) {
+      r.slot0.push_back((int32_t)num_slots);
+      for (int c = 0; c < r.nchunks; ++c) {
+        for (int t = 0; t < r.tiles; ++t) {
+          Tile x{};
+          x.item.b = r.b0;
+          x.item.hk = hk;
+          x.item.q_row0 = (int32_t)(r.q_row + (int64_t)t * r.tq);
+          x.item.q_i0 = t * r.tq;
+          x.item.n_q = std::min(r.tq, r.tokens - t * r.tq);
+          // (each query as the one query of its row: it sees every key of the prefix)
+          x.item.lq = 1;
+          x.item.lk = r.keys;
+          x.item.kv_begin = c * r.chunk;
+          x.item.kv_end = std::min(r.keys, (c + 1) * r.chunk);
+          x.item.kind = r.dec ? kDecode : kPrefill;
+          x.item.partial = (int32_t)num_slots;
+          x.item.nh = G;  // (h0 = 0: groups of up to 64 heads)
+          x.item.prefix = 1;
+          const int keys = x.item.kv_end - x.item.kv_begin;
+          x.cost = r.dec ? decode_cost(keys, D, esize)
+                         : std::max(decode_cost(keys, D, esize), prefill_cost(keys, prefill_rows, D));
+          tiles.push_back(x);
+          num_slots += r.tile_slots;
+          if (r.dec) ++n_dec; else ++n_pre;
+        }
+      }
+    }
+  }
+  q_row = 0;
   for (int b = 0; b < B; ++b) {
     int lq = h_q_lens[b], lc = h_cache_lens[b], ln = h_new_lens ? h_new_lens[b] : 0;
     int lk = lc + ln;
@@ -208,11 +340,14 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
         const int h0 = dec ? 0 : sg * nh_tc;
         const int nh = dec ? G : std::min(nh_tc, G - h0);
         if (splittable(lq)) {
-          // one query tile (all lq tokens), possibly cut into KV chunks
-          const int nchunks = nchunks_of(lk);
+          // one query tile (all lq tokens), possibly cut into KV chunks; with a
+          // shared prefix the keys past it, always into partials
+          const int first = shared[b];
+          const bool part = first > 0;
+          const int nchunks = lk > first || !part ? nchunks_of(lk - first) : 0;
           const int rows = lq * nh;
           const int stride = (rows + kDecodeRows - 1) / kDecodeRows;  // 16-row partial slots per chunk
-          const int64_t slot0 = nchunks > 1 ? num_slots : -1;
+          const int64_t slot0 = nchunks > 1 || part ? num_slots : -1;
           for (int c = 0; c < nchunks; ++c) {
             Tile t{};
             t.item.b = b;
@@ -222,10 +357,10 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
             t.item.n_q = lq;
             t.item.lq = lq;
             t.item.lk = lk;
-            t.item.kv_begin = (int32_t)std::min<int64_t>((int64_t)c * chunk, lk);
-            t.item.kv_end = (int32_t)std::min<int64_t>((int64_t)(c + 1) * chunk, lk);
+            t.item.kv_begin = (int32_t)std::min<int64_t>(first + (int64_t)c * chunk, lk);
+            t.item.kv_end = (int32_t)std::min<int64_t>(first + (int64_t)(c + 1) * chunk, lk);
             t.item.kind = dec ? kDecode : kPrefill;
-            t.item.partial = nchunks > 1 ? (int32_t)(num_slots + (int64_t)c * stride) : -1;
+            t.item.partial = nchunks > 1 || part ? (int32_t)(num_slots + (int64_t)c * stride) : -1;
             t.item.h0 = h0;
             t.item.nh = nh;
             const int keys = t.item.kv_end - t.item.kv_begin;
@@ -234,7 +369,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
             tiles.push_back(t);
             if (dec) ++n_dec; else ++n_pre;
           }
-          if (nchunks > 1) {
+          if (nchunks > 1 || part) {
             CombineItem ci{};
             ci.b = b;
             ci.q_row0 = (int32_t)q_row;
@@ -245,6 +380,15 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
             ci.slot_stride = stride;
             ci.h0 = h0;
             ci.nh = nh;
+            if (part) {
+              const PrefixRun& r = runs[run_of[b]];
+              ci.p_nsplit = r.nchunks;
+              ci.p_slot0 = r.slot0[hk];
+              ci.p_chunk_slots = r.tiles * r.tile_slots;
+              ci.p_tq = r.tq;
+              ci.p_tile_slots = r.tile_slots;
+              ci.p_tok0 = run_tok[b];
+            }
             combines.push_back(ci);
             num_slots += (int64_t)nchunks * stride;
           }
@@ -334,6 +478,8 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   off = align_up(off + sizeof(CombineItem) * (size_t)std::max<size_t>(1, combines.size()), 256);
   L.plan_lc = off;
   off = align_up(off + sizeof(int32_t) * (size_t)std::max(1, B), 256);
+  L.plan_min = off;
+  if (!runs.empty()) off = align_up(off + sizeof(int32_t) * (size_t)std::max(1, B), 256);
   size_t image_bytes = off;
   L.partial_o = off;
   off = align_up(off + sizeof(float) * (size_t)num_slots * kDecodeRows * D, 256);
@@ -367,6 +513,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   plan->num_items = num_items;
   plan->num_combine = (int32_t)combines.size();
   plan->dynamic = dynamic ? 1 : 0;
+  plan->shared = runs.empty() ? 0 : 1;
 
   WorkItem* items = (WorkItem*)(plan->image + L.items);
   int32_t* cta_begin = (int32_t*)(plan->image + L.cta_begin);
@@ -381,6 +528,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   if (!combines.empty()) memcpy(plan->image + L.combine, combines.data(), combines.size() * sizeof(CombineItem));
   int32_t* lc = (int32_t*)(plan->image + L.plan_lc);
   for (int b = 0; b < B; ++b) lc[b] = h_cache_lens[b];
+  if (plan->shared) memcpy(plan->image + L.plan_min, least.data(), sizeof(int32_t) * (size_t)B);
 
   *out_plan = plan;
   *out_workspace_bytes = L.total;
@@ -389,16 +537,41 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
 
 }  // namespace
 
+namespace {
+
+// make_plan for the C entries: what the containers throw becomes a status.
+template <class... Args>
+pkv_status make_plan_noexcept(Args... args) noexcept {
+  try {
+    return make_plan(args...);
+  } catch (const std::exception&) {
+    return fail(PKV_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
+}  // namespace
+
 extern "C" pkv_status pkv_plan(const pkv_problem* problem, const int32_t* h_q_lens,
                                const int32_t* h_cache_lens, const int32_t* h_new_lens,
                                int32_t num_sms, pkv_plan_t* out_plan, size_t* out_workspace_bytes) {
-  return make_plan(problem, h_q_lens, h_cache_lens, h_new_lens, num_sms, false, out_plan, out_workspace_bytes);
+  return make_plan_noexcept(problem, h_q_lens, h_cache_lens, h_new_lens, num_sms, false, nullptr, out_plan, out_workspace_bytes);
 }
 
 extern "C" pkv_status pkv_plan_decode_dynamic(const pkv_problem* problem, const int32_t* h_q_lens,
                                               const int32_t* h_max_cache_lens, const int32_t* h_new_lens,
                                               int32_t num_sms, pkv_plan_t* out_plan, size_t* out_workspace_bytes) {
-  return make_plan(problem, h_q_lens, h_max_cache_lens, h_new_lens, num_sms, true, out_plan, out_workspace_bytes);
+  return make_plan_noexcept(problem, h_q_lens, h_max_cache_lens, h_new_lens, num_sms, true, nullptr, out_plan,
+                   out_workspace_bytes);
+}
+
+extern "C" pkv_status pkv_plan_shared_prefix(const pkv_problem* problem, const int32_t* h_q_lens,
+                                             const int32_t* h_cache_lens, const int32_t* h_new_lens,
+                                             int32_t num_groups, const int32_t* h_group_starts,
+                                             const int32_t* h_prefix_lens, int32_t dynamic, int32_t num_sms,
+                                             pkv_plan_t* out_plan, size_t* out_workspace_bytes) {
+  const SharedPrefixes groups{num_groups, h_group_starts, h_prefix_lens};
+  return make_plan_noexcept(problem, h_q_lens, h_cache_lens, h_new_lens, num_sms, dynamic != 0, &groups, out_plan,
+                   out_workspace_bytes);
 }
 
 extern "C" pkv_status pkv_plan_get_stats(pkv_plan_t plan, pkv_plan_stats* s) {

@@ -281,7 +281,7 @@ def test_qk_norm_rope(pkv, gpu, d, rot, interleaved, norm, tokens, hq, hkv):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("tokens", [401, 701])       # two, four heads a lane
-@pytest.mark.parametrize("d,hq,hkv,interleaved", [(64, 66, 19, False), (128, 33, 9, True), (256, 17, 5, False)])
+@pytest.mark.parametrize("d,hq,hkv,interleaved", [(64, 66, 22, False), (128, 33, 11, True), (256, 15, 5, False)])
 def test_many_rows(pkv, gpu, tokens, d, hq, hkv, interleaved):
     """The splits of heads that larger calls take, at head counts that do not fill them; alone and into the cache."""
     torch = gpu
