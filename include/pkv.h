@@ -221,7 +221,8 @@ pkv_status pkv_plan_decode_dynamic(const pkv_problem* problem, const int32_t* h_
  * fit one tile (as for pkv_plan_decode_dynamic), or (causal) do not all see the
  * whole prefix, are planned as without it, and so is a group whose common tiles
  * (16 rows, else 128 / (Hq/Hkv) query tokens each) would be no fewer than its
- * sequences.
+ * sequences.  always = 0: prefixes are shared where a model of the call's time
+ * says that it pays (not for a few sequences on a short prefix); 1: always.
  * dynamic = 0: lengths as in pkv_plan; 1: as in pkv_plan_decode_dynamic
  * (h_cache_lens are bounds, the prefixes are fixed; a call whose
  * cache_seqlens[b] is below its prefix records PKV_ERR_PLAN_MISMATCH).
@@ -231,8 +232,8 @@ pkv_status pkv_plan_decode_dynamic(const pkv_problem* problem, const int32_t* h_
 pkv_status pkv_plan_shared_prefix(const pkv_problem* problem, const int32_t* h_q_lens,
                                   const int32_t* h_cache_lens, const int32_t* h_new_lens,
                                   int32_t num_groups, const int32_t* h_group_starts,
-                                  const int32_t* h_prefix_lens, int32_t dynamic, int32_t num_sms,
-                                  pkv_plan_t* out_plan, size_t* out_workspace_bytes);
+                                  const int32_t* h_prefix_lens, int32_t always, int32_t dynamic,
+                                  int32_t num_sms, pkv_plan_t* out_plan, size_t* out_workspace_bytes);
 
 /* Copies the plan's work list into the caller's device workspace on `stream`
  * (asynchronously; the host copy stays valid until pkv_plan_destroy) and clears

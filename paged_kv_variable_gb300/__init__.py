@@ -104,7 +104,7 @@ def lib() -> ctypes.CDLL:
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         L.pkv_plan.argtypes = [ctypes.POINTER(Problem), vp, vp, vp, i32, ctypes.POINTER(vp), ctypes.POINTER(sz)]
         L.pkv_plan_decode_dynamic.argtypes = L.pkv_plan.argtypes
-        L.pkv_plan_shared_prefix.argtypes = [ctypes.POINTER(Problem), vp, vp, vp, i32, vp, vp, i32, i32,
+        L.pkv_plan_shared_prefix.argtypes = [ctypes.POINTER(Problem), vp, vp, vp, i32, vp, vp, i32, i32, i32,
                                              ctypes.POINTER(vp), ctypes.POINTER(sz)]
         L.pkv_plan_upload.argtypes = [vp, vp, sz, vp]
         L.pkv_plan_get_stats.argtypes = [vp, ctypes.POINTER(PlanStats)]
@@ -281,12 +281,12 @@ class Plan:
         ws = ctypes.c_size_t()
         lens = (ctypes.byref(problem), self._q.ctypes.data, self._c.ctypes.data,
                 None if self._n is None else self._n.ctypes.data)
-        if shared is not None:  # (group_starts, prefix_lens)
-            starts, prefixes = (np.ascontiguousarray(x, dtype=np.int32) for x in shared)
+        if shared is not None:  # (group_starts, prefix_lens, always)
+            starts, prefixes = (np.ascontiguousarray(x, dtype=np.int32) for x in shared[:2])
             if len(starts) != len(prefixes) + 1:
                 raise ValueError(f"{len(prefixes)} prefix_lens need {len(prefixes) + 1} group_starts, got {len(starts)}")
             _check(lib().pkv_plan_shared_prefix(*lens, len(prefixes), starts.ctypes.data, prefixes.ctypes.data,
-                                                int(dynamic), int(num_sms), ctypes.byref(h), ctypes.byref(ws)))
+                                                int(bool(shared[2])), int(dynamic), int(num_sms), ctypes.byref(h), ctypes.byref(ws)))
         else:
             fn = lib().pkv_plan_decode_dynamic if dynamic else lib().pkv_plan
             _check(fn(*lens, int(num_sms), ctypes.byref(h), ctypes.byref(ws)))
@@ -339,15 +339,17 @@ def plan_decode_dynamic(problem: Problem, q_lens, max_cache_lens, new_lens=None,
 
 
 def plan_shared_prefix(problem: Problem, q_lens, cache_lens, new_lens=None, *, group_starts, prefix_lens,
-                       dynamic: bool = False, num_sms: Optional[int] = None) -> Plan:
+                       always: bool = False, dynamic: bool = False, num_sms: Optional[int] = None) -> Plan:
     """A plan for groups of consecutive sequences (group g: group_starts[g] ..
     group_starts[g+1] - 1) whose first prefix_lens[g] tokens lie in the same
-    pages: the prefix is attended once for the whole group.  dynamic: as
-    ``plan_decode_dynamic`` (cache_lens are bounds)."""
+    pages: the prefix is attended once for the whole group, where that is expected
+    to be faster (always: in any case).  dynamic: as ``plan_decode_dynamic``
+    (cache_lens are bounds)."""
     if num_sms is None:
         import torch
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
-    return Plan(problem, q_lens, cache_lens, new_lens, num_sms, dynamic=dynamic, shared=(group_starts, prefix_lens))
+    return Plan(problem, q_lens, cache_lens, new_lens, num_sms, dynamic=dynamic,
+                shared=(group_starts, prefix_lens, always))
 
 
 def attn_varlen_kvcache_fwd(problem: Problem, args: FwdArgs, plan_: Plan, workspace, stream=None) -> None:

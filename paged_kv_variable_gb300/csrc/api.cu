@@ -515,9 +515,32 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
   // across a profiling event, which must see the kernels in order, nor over a
   // rotating append, whose queries the attention reads from its start.
   const bool overlap = plan->num_prefill_items == 0;
-  e = launch_attention(p, tk, tv, tq, plan->num_ctas, pr.head_dim, pr.cache_dtype == PKV_FP8_E4M3,
-                       plan->num_prefill_items > 0, plan->num_decode_items > 0,
-                       overlap && plan->total_new > 0 && !rope && !g_ev_start, s);
+  const bool fp8 = pr.cache_dtype == PKV_FP8_E4M3;
+  const bool append_overlaps = plan->total_new > 0 && !rope && !g_ev_start;
+  if (plan->num_ctas_tc > 0) {
+    // A plan with shared prefixes and both kinds of tiles: the tensor-core tiles
+    // on num_ctas_tc SMs and the decode tiles on the others, each in the
+    // instance made for them, the second launch overlapping the first and ending
+    // only after it.
+    AttnParams pd = p;
+    pd.cta_begin += plan->num_ctas_tc;
+    const int dec_ctas = plan->num_ctas - plan->num_ctas_tc;
+    if (plan->dec_first) {
+      // the tensor-core tiles are all over prefixes, which no append writes
+      e = launch_attention(pd, tk, tv, tq, dec_ctas, pr.head_dim, fp8, false, true, append_overlaps, s);
+      if (e == cudaSuccess)
+        e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, true, s);
+    } else {
+      // the append is complete before the first launch starts
+      e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, false, s);
+      pd.dep_late = 1;
+      if (e == cudaSuccess)
+        e = launch_attention(pd, tk, tv, tq, dec_ctas, pr.head_dim, fp8, false, true, true, s);
+    }
+  } else {
+    e = launch_attention(p, tk, tv, tq, plan->num_ctas, pr.head_dim, fp8, plan->num_prefill_items > 0,
+                         plan->num_decode_items > 0, overlap && append_overlaps, s);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   if (g_ev_stop && (e = record_profile_event(g_ev_stop, s)) != cudaSuccess) return cuda_fail(e, "profile event");
 
@@ -533,7 +556,8 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
     cp.lse = p.lse;
     cp.total_q = p.total_q;
     cp.G = p.G;
-    e = plan->shared ? launch_combine_shared(cp, plan->num_combine, pr.head_dim, overlap && !g_ev_stop, s)
+    e = plan->shared ? launch_combine_shared(cp, plan->num_combine, plan->max_combine_rows, pr.head_dim,
+                                             overlap && !g_ev_stop, s)
                      : launch_combine(cp, plan->num_combine, pr.head_dim, overlap && !g_ev_stop, s);
     if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   }

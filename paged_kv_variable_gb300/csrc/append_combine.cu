@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kSharedCombineThreads) combine_shared_kernel(c
   const int lane = threadIdx.x & 31;
   const int rows = ci.n_q * ci.nh, parts = ci.p_nsplit + ci.nsplit;
   grid_dep_wait();  // the partials come from the attention kernel launched just before
-  for (int row = threadIdx.x >> 5; row < rows; row += kSharedCombineThreads / 32) {
+  const int row = blockIdx.y * (kSharedCombineThreads / 32) + (threadIdx.x >> 5);
+  if (row < rows) {
     // partial row of part 0 of each kind, and the rows between its parts
     const int tok = row / ci.nh, g = row - tok * ci.nh;
     const int pt = ci.p_tok0 + tok;
@@ -269,14 +270,14 @@ cudaError_t launch_combine(const CombineParams& p, int num_items, int head_dim, 
                            : cudaLaunchKernelEx(&cfg, combine_kernel<64>, p);
 }
 
-cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int head_dim, bool overlap_prev,
-                                  cudaStream_t stream) {
+cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int max_rows, int head_dim,
+                                  bool overlap_prev, cudaStream_t stream) {
   if (num_items == 0) return cudaSuccess;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)num_items);
+  cfg.gridDim = dim3((unsigned)num_items, (unsigned)((max_rows + kSharedCombineThreads / 32 - 1) / (kSharedCombineThreads / 32)));
   cfg.blockDim = dim3((unsigned)kSharedCombineThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = stream;

@@ -246,6 +246,7 @@ __device__ __forceinline__ WorkItem q_tile(const WorkItem& w, int q, bool causal
   v.q_i0 = w.q_i0 + q * tq;
   v.q_row0 = w.q_row0 + q * tq;
   v.n_q = max(0, min(tq, w.n_q - q * tq));
+  if (w.partial >= 0) v.partial = w.partial + q * (kPrefillRowsTc / kDecodeRows);
   if (v.n_q == 0)
     v.kv_end = v.kv_begin;
   else if (causal)
@@ -507,7 +508,7 @@ __device__ void producer(const AttnParams& p, const CUtensorMap* tm_kv, const CU
           slot = j0;
         }
       }
-      if (!dep_done && t0 + kTile > lc_old && lc_old < w.lk) {
+      if (!dep_done && !p.dep_late && t0 + kTile > lc_old && lc_old < w.lk) {
         grid_dep_wait();
         dep_done = true;
       }

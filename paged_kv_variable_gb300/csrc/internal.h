@@ -114,6 +114,9 @@ struct WorkspaceLayout {
 struct pkv_plan_s {
   pkv_problem problem;
   int32_t num_ctas;
+  int32_t num_ctas_tc;  // > 0: the first of them run tensor-core tiles, in a launch of their own
+  int32_t dec_first;    // the decode tiles' launch comes first
+  int32_t max_combine_rows;  // rows of the largest split unit
   int32_t num_slots;
   int32_t total_q;
   int32_t total_new;

@@ -99,6 +99,7 @@ struct AttnParams {
   const int32_t* plan_min;  // nullable: least cache lengths of a dynamic plan (its shared prefixes)
   int32_t batch;
   int32_t dynamic;     // plan_lc holds bounds; the cache lengths come from cache_seqlens
+  int32_t dep_late;    // the append came before the kernel this one overlaps: appended rows are there
 };
 
 // Start of sequence b's page list, and how many pages it has (-1: unchecked).
@@ -123,8 +124,8 @@ cudaError_t launch_rope_kv_append(const RopeParams& p, int head_dim, bool fp8, c
 cudaError_t launch_combine(const CombineParams& p, int num_items, int head_dim, bool overlap_prev,
                            cudaStream_t stream);
 // the same for plans with shared prefixes (parts over the prefix and over each sequence's own keys)
-cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int head_dim, bool overlap_prev,
-                                  cudaStream_t stream);
+cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int max_rows, int head_dim,
+                                  bool overlap_prev, cudaStream_t stream);
 cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const CUtensorMap& tm_q, int num_ctas, int head_dim, bool fp8, bool has_prefill,
                              bool has_decode, bool overlap_prev, cudaStream_t stream);

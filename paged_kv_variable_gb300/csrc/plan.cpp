@@ -37,6 +37,7 @@ struct SharedPrefixes {
   int32_t num_groups;
   const int32_t* starts;  // [num_groups + 1]
   const int32_t* prefix_lens;
+  bool always;  // shared whether or not the time model says that it pays
 };
 
 // Consecutive sequences whose queries attend the same `keys` first keys in
@@ -48,6 +49,7 @@ struct PrefixRun {
   int keys;       // shared keys, a whole number of pages
   bool dec;       // all rows in one warp-MMA tile
   int tq, tiles;  // query tokens a tile, tiles
+  int per_item;   // tiles an item holds (two where an item's query tiles share its K/V tiles)
   int nchunks, chunk;
   int tile_slots;             // partial slots of a tile
   std::vector<int32_t> slot0;  // first partial slot of each kv head
@@ -60,6 +62,136 @@ struct PrefixRun {
 // at 1.2 times and 0.442 at twice it; prefill-only batches do not move.)
 double decode_cost(int keys, int d, int esize) { return 64.0 + keys * (2.0 * d * esize) / 512.0; }
 double prefill_cost(int keys, int rows, int d) { return 256.0 + keys * (rows * d * 4.0) / 65536.0; }
+
+// Time model (us) of the launches of a plan with shared prefixes, from
+// measurements on a GB300: what the choice of SMs and chunks below balances.
+struct TimeModel {
+  double tile1, tile2;  // a tensor-core K/V tile of 128 keys, one and two query tiles
+  double sm_rate, hbm;  // decode tiles: bytes a us of one SM and of all
+  int cps;              // decode CTAs an SM
+  double key_bytes;
+  TimeModel(int d, bool fp8) {
+    if (fp8) {
+      tile1 = d == 64 ? 2.0 : d == 128 ? 3.0 : 4.0;
+      tile2 = d == 64 ? 2.6 : 3.8;
+      sm_rate = d == 64 ? 20e3 : d == 128 ? 31e3 : 25e3;
+      hbm = sm_rate * 152;
+    } else {
+      tile1 = tile2 = d == 64 ? 1.0 : d == 128 ? 1.1 : 2.2;
+      sm_rate = d == 64 ? 38e3 : 54e3;
+      hbm = d == 64 ? 5.4e6 : 6.1e6;
+    }
+    cps = (fp8 ? d <= 128 : d == 64) ? 2 : 1;
+    key_bytes = 2.0 * d * (fp8 ? 1 : 2);
+  }
+  static constexpr double kItemTc = 4.5;   // start and end of a tensor-core chunk
+  static constexpr double kItemDec = 1.2;  // of a decode item
+  static constexpr double kParts = 4.0;    // the combine kernel
+  static constexpr double kPartRate = 5e6;  // bytes a us of partials written and read
+
+  // `keys` of decode work in `units` units, the longest of `longest` keys
+  double decode(int64_t keys, int64_t units, int64_t longest, int sms) const {
+    if (keys == 0) return 0.0;
+    if (sms <= 0) return HUGE_VAL;
+    const double chunk = std::max(512.0, (double)keys / (2.0 * sms));
+    const double items = std::max((double)units, (double)keys / chunk);
+    const double bytes = keys * key_bytes;
+    const double one = std::min((double)longest, chunk) * key_bytes / (sm_rate / cps) + kItemDec;
+    return std::max({bytes / hbm, (bytes / sm_rate + items * kItemDec / cps) / sms, one});
+  }
+};
+
+// The decode work of a batch (with each sequence's first shared[b] keys taken out).
+struct DecodeWork {
+  int64_t keys = 0, units = 0, longest = 0;
+  void add(int64_t n, int64_t count) {
+    keys += n * count;
+    units += count;
+    longest = std::max(longest, n);
+  }
+};
+
+// What a plan with shared prefixes takes by the model: SMs of the tensor-core
+// tiles, keys a chunk of theirs, and the time.
+struct SplitChoice {
+  int sms_tc;
+  int64_t chunk;
+  double time;
+};
+
+SplitChoice choose_split(const pkv_problem& p, const std::vector<PrefixRun>& runs, const int32_t* q_lens,
+                         const int32_t* cache_lens, const int32_t* new_lens, const int32_t* shared, int num_sms,
+                         int n_sub, int tq, int dec_rows) {
+  const int G = p.num_heads_q / p.num_heads_kv, D = p.head_dim;
+  const TimeModel tm(D, p.cache_dtype == PKV_FP8_E4M3);
+  DecodeWork dec;
+  int64_t longest = 0;  // of the units that tensor-core tiles may cut
+  double fixed = 0;     // tensor-core tiles that are not cut
+  int64_t fixed_items = 0;
+  std::vector<int64_t> cut;  // keys of each sequence whose tensor-core tiles may be cut
+  double own_rows = 0;  // rows of the units in parts over their own keys
+  for (const PrefixRun& r : runs) {
+    if (r.dec)
+      dec.add(r.keys, p.num_heads_kv);
+    else
+      longest = std::max<int64_t>(longest, r.keys);
+  }
+  for (int b = 0; b < p.batch; ++b) {
+    const int lq = q_lens[b];
+    if (lq == 0) continue;
+    const int64_t keys = (int64_t)cache_lens[b] + (new_lens ? new_lens[b] : 0) - shared[b];
+    if ((int64_t)lq * G <= dec_rows) {
+      dec.add(keys, p.num_heads_kv);
+    } else if (lq <= tq) {
+      longest = std::max(longest, keys);
+      cut.push_back(keys);
+    } else {
+      const int64_t n = (int64_t)p.num_heads_kv * n_sub * ((lq + tq - 1) / tq);
+      fixed += n * (tm.kItemTc + keys / 128.0 * tm.tile1);
+      fixed_items += n;
+    }
+    if (shared[b] > 0) own_rows += (double)lq * p.num_heads_q;
+  }
+  const double row_bytes = 2.0 * D * sizeof(float);  // written and read
+  SplitChoice best{num_sms, 1 << 30, HUGE_VAL};
+  for (int64_t k = 2;; k += std::max<int64_t>(1, k / 4)) {
+    const int64_t ch = k * kKvTile;
+    double sum = fixed, most = 0, rows = own_rows;
+    int64_t items = fixed_items;
+    auto add = [&](int64_t keys, int64_t n, double tile) {
+      if (keys <= 0 || n <= 0) return;
+      const int64_t c = (keys + ch - 1) / ch, each = ((keys + c - 1) / c + kKvTile - 1) / kKvTile;
+      const double t = tm.kItemTc + each * tile;
+      items += c * n;
+      sum += c * n * t;
+      most = std::max(most, t);
+    };
+    for (const PrefixRun& r : runs) {
+      rows += (double)r.tokens * p.num_heads_q * (r.dec ? 1 : (r.keys + ch - 1) / ch);
+      if (r.dec) continue;
+      add(r.keys, (int64_t)p.num_heads_kv * (r.tiles / r.per_item), r.per_item == 2 ? tm.tile2 : tm.tile1);
+      add(r.keys, (int64_t)p.num_heads_kv * (r.tiles % r.per_item), tm.tile1);
+    }
+    for (int64_t keys : cut) add(keys, (int64_t)p.num_heads_kv * n_sub, tm.tile1);
+    auto consider = [&](int sms) {
+      const double tc = items == 0 ? 0.0
+                                   : std::max({most, sum / sms, (double)((items + sms - 1) / sms) * sum / items});
+      // (with no prefix shared: one launch, in which both kinds share every SM)
+      const double t = runs.empty() ? tc + tm.decode(dec.keys, dec.units, dec.longest, num_sms)
+                       : std::max(tc, tm.decode(dec.keys, dec.units, dec.longest, items ? num_sms - sms : num_sms)) +
+                             tm.kParts + rows * row_bytes / tm.kPartRate;
+      if (t < best.time) best = {sms, ch, t};
+    };
+    if (dec.keys == 0 || items == 0 || runs.empty() || num_sms < 2) {
+      consider(num_sms);
+    } else {
+      for (int sms = std::max(1, num_sms / 38); sms < num_sms; sms += std::max(1, num_sms / 38)) consider(sms);
+      if (items < num_sms) consider((int)items);
+    }
+    if (ch >= longest) break;
+  }
+  return best;
+}
 
 }  // namespace
 
@@ -165,8 +297,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
         if (run.tiles < members && keys > 0) {
           run.keys = keys;
           run.tile_slots = run.dec ? 1 : kPrefillRowsTc / kDecodeRows;
-          any_decode |= run.dec;
-          any_prefill |= !run.dec;
+          run.per_item = run.dec ? 1 : prefill_q_tiles(D, p.cache_dtype == PKV_FP8_E4M3);
           for (int b = run.b0, n = members; n > 0; ++b) {
             if (h_q_lens[b] == 0) continue;
             shared[b] = keys;
@@ -200,13 +331,32 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
       close_run();
     }
   }
-  const int tq_item = tq_prefill * (any_decode ? 1 : prefill_q_tiles(D, p.cache_dtype == PKV_FP8_E4M3));
+  // Sharing pays once the keys it saves outweigh the parts' combine kernel (four
+  // sequences on 512 keys: 11.5 us a call shared, 10.4 not; 64 on 2048: 42 and 98).
+  if (!runs.empty() && !groups->always) {
+    const std::vector<int32_t> none(B, 0);
+    const double with = choose_split(p, runs, h_q_lens, h_cache_lens, h_new_lens, shared.data(), num_sms, n_sub,
+                                     tq_prefill, dec_rows).time;
+    const double without =
+        choose_split(p, {}, h_q_lens, h_cache_lens, h_new_lens, none.data(), num_sms, n_sub, tq_prefill, dec_rows).time;
+    if (with >= without) {
+      runs.clear();
+      shared.assign(B, 0);
+    }
+  }
+  // (plans with shared prefixes launch their decode tiles apart)
+  const bool sp = !runs.empty();
+  const int tq_item = tq_prefill * (any_decode && !sp ? 1 : prefill_q_tiles(D, p.cache_dtype == PKV_FP8_E4M3));
+  for (const PrefixRun& r : runs) {
+    any_decode |= r.dec;
+    any_prefill |= !r.dec;
+  }
   // decode-only plans over an fp8 cache at head dims up to 128, or a bf16 one
   // at head dim 64 (rows of 128 bytes), run two CTAs an SM
-  const bool two_ctas = (p.cache_dtype == PKV_FP8_E4M3 ? D <= 128 : D == 64) && !any_prefill;
+  const bool two_ctas = (p.cache_dtype == PKV_FP8_E4M3 ? D <= 128 : D == 64) && (!any_prefill || sp);
   const int cps = two_ctas ? 2 : 1;
 
-  int64_t total_q = 0, total_new = 0, total_split_keys = 0;
+  int64_t total_q = 0, total_new = 0, total_split_keys = 0, total_dec_keys = 0;
   for (int b = 0; b < B; ++b) {
     int lq = h_q_lens[b], lc = h_cache_lens[b], ln = h_new_lens ? h_new_lens[b] : 0;
     if (lq < 0 || lc < 0 || ln < 0) return fail(PKV_ERR_INVALID_ARG, "negative length at sequence %d", b);
@@ -221,9 +371,10 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
                   std::max(tq_prefill, dec_rows / G));
     if (lq > 0 && splittable(lq))
       total_split_keys += (int64_t)(lc + ln - shared[b]) * p.num_heads_kv * (is_decode(lq) ? 1 : n_sub);
+    if (is_decode(lq) && lq > 0) total_dec_keys += (int64_t)(lc + ln - shared[b]) * p.num_heads_kv;
   }
   for (const PrefixRun& r : runs)
-    total_split_keys += (int64_t)r.keys * r.tiles * p.num_heads_kv;
+    if (r.dec) total_dec_keys += (int64_t)r.keys * p.num_heads_kv;
   if (total_q > INT32_MAX / 2 || total_new > INT32_MAX / 2)
     return fail(PKV_ERR_UNSUPPORTED, "total tokens too large");
 
@@ -233,31 +384,48 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   // against 60.9 us at 4, one of random lengths 61.7 against 64.9; the bf16
   // decode batch the same attention kernel and 100.4 against 101.8 us a call
   // (fewer partials to combine); the mixed batch 0.417 against 0.430 ms at 4.
-  auto chunk_for = [&](int64_t items_per_sm) {
-    const int64_t target = items_per_sm * num_sms;
-    const int64_t c = (total_split_keys + target - 1) / target;
+  auto chunk_for = [&](int64_t items_per_sm, int64_t keys, int sms) {
+    const int64_t target = items_per_sm * sms;
+    const int64_t c = (keys + target - 1) / target;
     return std::max<int64_t>(512, (c + kKvTile - 1) / kKvTile * kKvTile);
   };
+  // Plans with shared prefixes: the SMs that the tensor-core tiles get (the
+  // decode tiles run on the others at the same time), and the chunks.
+  int sms_tc = num_sms;
+  int64_t chunk_tc = 1 << 30;
+  if (sp) {
+    const SplitChoice c = choose_split(p, runs, h_q_lens, h_cache_lens, h_new_lens, shared.data(), num_sms, n_sub,
+                                       tq_prefill, dec_rows);
+    sms_tc = c.sms_tc;
+    chunk_tc = c.chunk;
+  }
+  const int sms_dec = sp && any_prefill ? std::max(1, num_sms - sms_tc) : num_sms;
+  const int64_t dec_keys = sp ? total_dec_keys : total_split_keys;
   int64_t chunk = 1 << 30;
-  if (total_split_keys > 0) chunk = chunk_for(any_prefill ? 4 : 2);
+  if (dec_keys > 0) chunk = chunk_for(any_prefill && !sp ? 4 : 2, dec_keys, sms_dec);
   // A decode-only plan whose units are placed as evenly whole (one item an SM
   // as the target) as in chunks of the half is not split at all: no partials
   // and no combine kernel (the bf16 decode batch: 98.1 against 100.3 us a
   // call, the same attention kernel).  Judged on the model costs of a
   // longest-first placement; batches with a few long sequences stay split.
-  if (!any_prefill && runs.empty() && total_split_keys > 0) {
-    const int ctas = num_sms * cps;
+  if ((!any_prefill || sp) && dec_keys > 0) {
+    const int ctas = sms_dec * cps;
     std::vector<double> c, load;
     c.reserve((size_t)B * 4);
     load.reserve((size_t)ctas);
     auto busiest = [&](int64_t ch) {  // the longest-first placement's largest CTA cost
       c.clear();
       for (int b = 0; b < B; ++b) {  // one cost per chunk; every kv head has the same
-        if (h_q_lens[b] == 0) continue;
-        const int lk = h_cache_lens[b] + (h_new_lens ? h_new_lens[b] : 0);
+        if (h_q_lens[b] == 0 || (sp && !is_decode(h_q_lens[b]))) continue;
+        const int lk = h_cache_lens[b] + (h_new_lens ? h_new_lens[b] : 0) - shared[b];
         const int n = lk <= ch ? 1 : (int)((lk + ch - 1) / ch);
         for (int k = 0; k < n; ++k)
           c.push_back(decode_cost((int)(std::min<int64_t>((int64_t)(k + 1) * ch, lk) - (int64_t)k * ch), D, esize));
+      }
+      for (const PrefixRun& r : runs) {
+        if (!r.dec) continue;
+        for (int64_t k = 0; k < r.keys; k += ch)
+          c.push_back(decode_cost((int)std::min<int64_t>(ch, r.keys - k), D, esize));
       }
       std::sort(c.begin(), c.end(), std::greater<double>());
       load.assign((size_t)ctas, 0.0);  // a min-heap over the CTA loads
@@ -269,13 +437,19 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
         }
       return *std::max_element(load.begin(), load.end());
     };
-    const int64_t whole = chunk_for(1);
+    const int64_t whole = chunk_for(1, dec_keys, sms_dec);
     if (whole != chunk && busiest(whole) <= 1.02 * busiest(chunk)) chunk = whole;
   }
-  auto nchunks_of = [&](int lk) { return lk <= chunk ? 1 : (int)((lk + chunk - 1) / chunk); };
-
+  // (plans with shared prefixes: the tensor-core units have chunks of their own)
+  auto chunk_of = [&](bool dec) { return dec || !sp ? chunk : chunk_tc; };
+  auto nchunks_of = [&](int lk, bool dec) {
+    const int64_t ch = chunk_of(dec);
+    return lk <= ch ? 1 : (int)((lk + ch - 1) / ch);
+  };
   for (PrefixRun& r : runs) {
-    r.chunk = (int)std::min<int64_t>(chunk, r.keys);
+    // chunks of nearly the same size
+    const int n = nchunks_of(r.keys, r.dec);
+    r.chunk = ((r.keys + n - 1) / n + kKvTile - 1) / kKvTile * kKvTile;
     r.nchunks = (r.keys + r.chunk - 1) / r.chunk;
   }
 
@@ -283,8 +457,8 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   for (int b = 0; b < B; ++b) {
     const int lq = h_q_lens[b], lk = h_cache_lens[b] + (h_new_lens ? h_new_lens[b] : 0);
     if (lq == 0) continue;
-    num_tiles_est += (int64_t)p.num_heads_kv * (is_decode(lq) ? nchunks_of(lk)
-                                                : (int64_t)n_sub * (splittable(lq) ? nchunks_of(lk)
+    num_tiles_est += (int64_t)p.num_heads_kv * (is_decode(lq) ? nchunks_of(lk, true)
+                                                : (int64_t)n_sub * (splittable(lq) ? nchunks_of(lk, false)
                                                                                    : (lq + tq_item - 1) / tq_item));
   }
   std::vector<Tile> tiles;
@@ -303,13 +477,14 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
     for (int hk = 0; hk < p.num_heads_kv; ++hk) {
       r.slot0.push_back((int32_t)num_slots);
       for (int c = 0; c < r.nchunks; ++c) {
-        for (int t = 0; t < r.tiles; ++t) {
+        for (int t = 0; t < r.tiles; t += r.per_item) {
+          const int nt = std::min(r.per_item, r.tiles - t);  // query tiles of the item
           Tile x{};
           x.item.b = r.b0;
           x.item.hk = hk;
           x.item.q_row0 = (int32_t)(r.q_row + (int64_t)t * r.tq);
           x.item.q_i0 = t * r.tq;
-          x.item.n_q = std::min(r.tq, r.tokens - t * r.tq);
+          x.item.n_q = std::min(nt * r.tq, r.tokens - t * r.tq);
           // (each query as the one query of its row: it sees every key of the prefix)
           x.item.lq = 1;
           x.item.lk = r.keys;
@@ -321,9 +496,9 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
           x.item.prefix = 1;
           const int keys = x.item.kv_end - x.item.kv_begin;
           x.cost = r.dec ? decode_cost(keys, D, esize)
-                         : std::max(decode_cost(keys, D, esize), prefill_cost(keys, prefill_rows, D));
+                         : std::max(decode_cost(keys, D, esize), prefill_cost(keys, nt * prefill_rows, D));
           tiles.push_back(x);
-          num_slots += r.tile_slots;
+          num_slots += nt * r.tile_slots;
           if (r.dec) ++n_dec; else ++n_pre;
         }
       }
@@ -344,7 +519,8 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
           // shared prefix the keys past it, always into partials
           const int first = shared[b];
           const bool part = first > 0;
-          const int nchunks = lk > first || !part ? nchunks_of(lk - first) : 0;
+          const int nchunks = lk > first || !part ? nchunks_of(lk - first, dec) : 0;
+          const int64_t chunk_u = chunk_of(dec);
           const int rows = lq * nh;
           const int stride = (rows + kDecodeRows - 1) / kDecodeRows;  // 16-row partial slots per chunk
           const int64_t slot0 = nchunks > 1 || part ? num_slots : -1;
@@ -357,8 +533,8 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
             t.item.n_q = lq;
             t.item.lq = lq;
             t.item.lk = lk;
-            t.item.kv_begin = (int32_t)std::min<int64_t>(first + (int64_t)c * chunk, lk);
-            t.item.kv_end = (int32_t)std::min<int64_t>(first + (int64_t)(c + 1) * chunk, lk);
+            t.item.kv_begin = (int32_t)std::min<int64_t>(first + (int64_t)c * chunk_u, lk);
+            t.item.kv_end = (int32_t)std::min<int64_t>(first + (int64_t)(c + 1) * chunk_u, lk);
             t.item.kind = dec ? kDecode : kPrefill;
             t.item.partial = nchunks > 1 || part ? (int32_t)(num_slots + (int64_t)c * stride) : -1;
             t.item.h0 = h0;
@@ -432,32 +608,47 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   // longest processing time first onto the least-loaded CTA (ties: the lowest
   // CTA index), found with a tournament tree over the CTAs' (load, index)
   // pairs; each CTA keeps its items in the order they were assigned
+  // (plans with shared prefixes: tensor-core tiles and decode tiles apart, on
+  // sms_tc and sms_dec SMs, the tensor-core CTAs first)
   const int num_items = (int)tiles.size();
-  const int num_ctas = std::max(1, std::min(num_sms * cps, num_items));
   std::vector<double> costs(num_items);
   for (int i = 0; i < num_items; ++i) costs[i] = tiles[i].cost;
   std::vector<int> order(num_items);
   for (int i = 0; i < num_items; ++i) order[i] = i;
   std::stable_sort(order.begin(), order.end(), [&](int a, int c) { return costs[a] > costs[c]; });
-  using Load = std::pair<double, int>;
-  int leaves = 1;
-  while (leaves < num_ctas) leaves *= 2;
-  const Load none{HUGE_VAL, INT32_MAX};
-  std::vector<Load> tree(2 * (size_t)leaves, none);  // node i: the lesser of nodes 2i and 2i+1
-  for (int c = 0; c < num_ctas; ++c) tree[leaves + c] = {0.0, c};
-  for (int i = leaves - 1; i >= 1; --i) tree[i] = std::min(tree[2 * i], tree[2 * i + 1]);
+  const bool apart = sp && n_dec > 0 && n_pre > 0;
+  const int num_tc = apart ? std::min(sms_tc, (int)n_pre) : 0;
+  const int num_ctas = apart ? num_tc + std::min(sms_dec * cps, (int)n_dec)
+                             : std::max(1, std::min(num_sms * (any_prefill ? 1 : cps), num_items));
   std::vector<int> cta_of(num_items), cta_count(num_ctas, 0);
-  for (int idx : order) {
-    const int c = tree[1].second;
-    cta_of[idx] = c;
-    ++cta_count[c];
-    int i = leaves + c;
-    tree[i].first += costs[idx];
-    for (i >>= 1; i >= 1; i >>= 1) tree[i] = std::min(tree[2 * i], tree[2 * i + 1]);
+  using Load = std::pair<double, int>;
+  std::vector<Load> loads;
+  auto assign = [&](int first, int ctas, auto&& takes) {
+    int leaves = 1;
+    while (leaves < ctas) leaves *= 2;
+    const Load none{HUGE_VAL, INT32_MAX};
+    std::vector<Load> tree(2 * (size_t)leaves, none);  // node i: the lesser of nodes 2i and 2i+1
+    for (int c = 0; c < ctas; ++c) tree[leaves + c] = {0.0, c};
+    for (int i = leaves - 1; i >= 1; --i) tree[i] = std::min(tree[2 * i], tree[2 * i + 1]);
+    for (int idx : order) {
+      if (!takes(idx)) continue;
+      const int c = tree[1].second;
+      cta_of[idx] = first + c;
+      ++cta_count[first + c];
+      int i = leaves + c;
+      tree[i].first += costs[idx];
+      for (i >>= 1; i >= 1; i >>= 1) tree[i] = std::min(tree[2 * i], tree[2 * i + 1]);
+    }
+    loads.insert(loads.end(), tree.begin() + leaves, tree.begin() + leaves + ctas);
+  };
+  if (apart) {
+    assign(0, num_tc, [&](int i) { return tiles[i].item.kind == kPrefill; });
+    assign(num_tc, num_ctas - num_tc, [&](int i) { return tiles[i].item.kind == kDecode; });
+  } else {
+    assign(0, num_ctas, [](int) { return true; });
   }
   double max_cost = 0, sum_cost = 0;
   int max_items = 0;
-  std::vector<Load> loads(tree.begin() + leaves, tree.begin() + leaves + num_ctas);
   std::sort(loads.begin(), loads.end());  // summed lightest first
   for (const Load& l : loads) {
     max_cost = std::max(max_cost, l.first);
@@ -499,6 +690,15 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   }
   plan->problem = p;
   plan->num_ctas = num_items > 0 ? num_ctas : 0;
+  plan->num_ctas_tc = num_tc;
+  // The decode tiles usually take longest, so their launch comes first; but two
+  // of their CTAs an SM would spread over every SM and leave the tensor-core
+  // CTAs none, and tensor-core tiles over appended keys would wait for them.
+  bool tc_prefix_only = true;
+  for (const Tile& t : tiles) tc_prefix_only &= t.item.kind == kDecode || t.item.prefix != 0;
+  plan->dec_first = apart && cps == 1 && tc_prefix_only;
+  plan->max_combine_rows = 0;
+  for (const CombineItem& c : combines) plan->max_combine_rows = std::max(plan->max_combine_rows, c.n_q * c.nh);
   plan->num_slots = (int32_t)num_slots;
   plan->total_q = (int32_t)total_q;
   plan->total_new = (int32_t)total_new;
@@ -567,9 +767,9 @@ extern "C" pkv_status pkv_plan_decode_dynamic(const pkv_problem* problem, const 
 extern "C" pkv_status pkv_plan_shared_prefix(const pkv_problem* problem, const int32_t* h_q_lens,
                                              const int32_t* h_cache_lens, const int32_t* h_new_lens,
                                              int32_t num_groups, const int32_t* h_group_starts,
-                                             const int32_t* h_prefix_lens, int32_t dynamic, int32_t num_sms,
-                                             pkv_plan_t* out_plan, size_t* out_workspace_bytes) {
-  const SharedPrefixes groups{num_groups, h_group_starts, h_prefix_lens};
+                                             const int32_t* h_prefix_lens, int32_t always, int32_t dynamic,
+                                             int32_t num_sms, pkv_plan_t* out_plan, size_t* out_workspace_bytes) {
+  const SharedPrefixes groups{num_groups, h_group_starts, h_prefix_lens, always != 0};
   return make_plan_noexcept(problem, h_q_lens, h_cache_lens, h_new_lens, num_sms, dynamic != 0, &groups, out_plan,
                    out_workspace_bytes);
 }

@@ -65,16 +65,16 @@ def test_refusals(pkv):
     import ctypes
     h, n = ctypes.c_void_p(), ctypes.c_size_t()
     lens = np.full(4, 100, np.int32)
-    assert L.pkv_plan_shared_prefix(problem(pkv), lens.ctypes.data, lens.ctypes.data, None, 1, None, None, 0, 4,
+    assert L.pkv_plan_shared_prefix(problem(pkv), lens.ctypes.data, lens.ctypes.data, None, 1, None, None, 0, 0, 4,
                                     h, n) == 1
-    assert L.pkv_plan_shared_prefix(problem(pkv), lens.ctypes.data, lens.ctypes.data, None, -1, None, None, 0, 4,
+    assert L.pkv_plan_shared_prefix(problem(pkv), lens.ctypes.data, lens.ctypes.data, None, -1, None, None, 0, 0, 4,
                                     h, n) == 1
 
 
 def test_placed_rows_refused(pkv):
     """q_rows > 0 (rows placed by the caller) is refused before anything is launched."""
     pl = pkv.plan_shared_prefix(problem(pkv), (1,) * 4, (2000,) * 4, None, group_starts=(0, 4), prefix_lens=(1600,),
-                                num_sms=4)
+                                always=True, num_sms=4)
     q, c = _Fake((4, 8, 128)), _Fake((1000, 16, 2, 128), ptr=1 << 24)
     i32, bt = _Fake((5,), "int32"), _Fake((4, 256), "int32")
     ws = _Fake((pl.workspace_bytes,), "uint8", ptr=1 << 28)
@@ -112,7 +112,7 @@ def test_plan_covers_every_key_once(pkv, i, dynamic):
     prob = problem(pkv, batch=B, num_heads_q=hq, num_heads_kv=hkv, head_dim=d, page_size=page, cache_dtype=dtype,
                    causal=causal, cache_capacity=cap)
     pl = pkv.plan_shared_prefix(prob, q, cache, new, group_starts=starts, prefix_lens=prefix, dynamic=dynamic,
-                                num_sms=8)
+                                always=True, num_sms=8)
     row_of = np.concatenate([[0], np.cumsum(q)])
     seq_of = np.repeat(np.arange(B), q)
     lk = np.array(cache) + (np.array(new) if new is not None else 0)
@@ -155,13 +155,28 @@ def test_plan_covers_every_key_once(pkv, i, dynamic):
         assert keys(pl) < keys(pkv.plan(prob, q, cache, new, num_sms=8))
 
 
+def test_shared_where_it_pays(pkv):
+    """A few sequences on a short prefix are planned as without it; many, or a long one, are not."""
+    def plans(B, prefix, sms=152, **kw):
+        prob = problem(pkv, batch=B, num_heads_q=32, num_heads_kv=8, cache_capacity=1 << 16, **kw)
+        args = (prob, [1] * B, [prefix + 40 + b for b in range(B)], None)
+        shared = pkv.plan_shared_prefix(*args, group_starts=[0, B], prefix_lens=[prefix], num_sms=sms)
+        return shared.items() != pkv.plan(*args, num_sms=sms).items()
+
+    for dtype in ("bf16", "fp8"):
+        assert not plans(4, 512, cache_dtype=dtype)
+        assert not plans(2, 128, cache_dtype=dtype)
+        assert plans(64, 2048, cache_dtype=dtype)
+        assert plans(4, 32768, cache_dtype=dtype)
+
+
 def test_nothing_to_share_equals_the_plain_plan(pkv):
     prob = problem(pkv)
     args = ((1, 2, 0, 300), (3000, 2000, 10, 400), (1, 2, 1, 300))
     plain = pkv.plan(prob, *args, num_sms=8)
     for starts, prefix in (([0], []), ([0, 4], [0]), ([0, 4], [9]), ([0, 1, 2, 4], [2000, 1000, 10]),
                            ([0, 1, 4], [0, 10])):
-        pl = pkv.plan_shared_prefix(prob, *args, group_starts=starts, prefix_lens=prefix, num_sms=8)
+        pl = pkv.plan_shared_prefix(prob, *args, group_starts=starts, prefix_lens=prefix, always=True, num_sms=8)
         assert pl.items() == plain.items()
 
 
@@ -171,7 +186,7 @@ class Shared:
     table of their group.  Slots that no token holds are NaN (bf16)."""
 
     def __init__(self, pkv, torch, seed, *, starts, prefix, own, q, new=None, hq=8, hkv=2, d=128, page=16, fp8=False,
-                 causal=True, q_scale=None, ragged=False, num_sms=None, dynamic=False, bound=0):
+                 causal=True, q_scale=None, ragged=False, num_sms=None, dynamic=False, bound=0, shares=True):
         rng = np.random.default_rng(seed)
         self.pkv, self.torch, self.fp8, self.causal, self.page, self.d, self.hq = pkv, torch, fp8, causal, page, d, hq
         B = len(q)
@@ -229,7 +244,11 @@ class Shared:
                                         cache_capacity=cap, num_pages=need, cache_dtype="fp8" if fp8 else "bf16",
                                         causal=causal, softmax_scale=d ** -0.5)
         self.plan = pkv.plan_shared_prefix(self.problem, self.q_lens, self.cache + bound, self.new,
-                                           group_starts=starts, prefix_lens=prefix, dynamic=dynamic, num_sms=num_sms)
+                                           group_starts=starts, prefix_lens=prefix, always=True, dynamic=dynamic,
+                                           num_sms=num_sms)
+        # shared: some tile holds rows of several sequences
+        first = np.repeat(np.arange(B), self.q_lens)
+        assert shares == any(first[it["q_row0"]] != first[it["q_row0"] + it["n_q"] - 1] for it in self.plan.items())
         self.ws = pkv.workspace_tensor(self.plan.workspace_bytes)
         self.plan.upload(self.ws)
 
@@ -301,7 +320,7 @@ CASES = dict(
     d256_few=dict(starts=[0, 2], prefix=[1100], own=[20, 30], q=[1] * 2, d=256, hq=8, hkv=2),
     mqa=dict(starts=[0, 10], prefix=[1100], own=rnd.integers(1, 900, 10), q=[1] * 10, hq=32, hkv=1),
     wide=dict(starts=[0, 3], prefix=[600], own=[5, 600, 77], q=[1] * 3, hq=60, hkv=1),
-    not_shared=dict(starts=[0, 3], prefix=[600], own=[5, 600, 77], q=[1] * 3, hq=200, hkv=1),      # head sub-groups
+    not_shared=dict(starts=[0, 3], prefix=[600], own=[5, 600, 77], q=[1] * 3, hq=200, hkv=1, shares=False),  # head sub-groups
     mha=dict(starts=[0, 40], prefix=[600], own=rnd.integers(1, 90, 40), q=[1] * 40, hq=3, hkv=3),
     page1=dict(starts=[0, 20], prefix=[333], own=rnd.integers(1, 90, 20), q=[1] * 20, page=1),
     page4=dict(starts=[0, 20], prefix=[335], own=rnd.integers(1, 90, 20), q=[1] * 20, page=4),
@@ -310,10 +329,12 @@ CASES = dict(
     page256=dict(starts=[0, 20], prefix=[800], own=rnd.integers(1, 900, 20), q=[1] * 20, page=256),
     ragged=dict(starts=[0, 20], prefix=[480], own=rnd.integers(1, 90, 20), q=[1] * 20, ragged=True),
     many_chunks=dict(starts=[0, 20], prefix=[20000], own=rnd.integers(1, 5000, 20), q=[1] * 20, hq=4, hkv=1),
+    full=dict(starts=[0, 64], prefix=[6000], own=rnd.integers(1, 1500, 64), q=[1] * 64, hq=32, hkv=8),
     one_sm=dict(starts=[0, 20], prefix=[900], own=rnd.integers(1, 400, 20), q=[1] * 20, num_sms=1),
+    few_sms=dict(starts=[0, 20], prefix=[1900], own=rnd.integers(1, 400, 20), q=[1] * 20, num_sms=7),
 )
 FP8 = ("few_rows", "one_tile", "two_tiles", "odd_tiles", "groups", "new_tokens", "long_run_inside", "prefix_only", "d64",
-       "d256", "mqa", "wide", "page4", "page24", "many_chunks")
+       "d256", "mqa", "wide", "page4", "page24", "many_chunks", "full", "one_sm", "few_sms")
 
 
 @pytest.mark.gpu
