@@ -316,9 +316,10 @@ extern "C" pkv_status pkv_qk_norm_rope(const pkv_qk_args* args, const pkv_rope_s
   if (st != PKV_OK) return st;
   if (a.num_tokens < 0 || a.num_heads_q < 0 || a.num_heads_kv < 0)
     return fail(PKV_ERR_INVALID_ARG, "negative token or head count");
+  if (a.num_tokens == 0) return PKV_OK;  // (empty tensors may have no address)
   if ((a.num_heads_q > 0) != (a.q != nullptr) || (a.num_heads_kv > 0) != (a.k != nullptr))
     return fail(PKV_ERR_INVALID_ARG, "heads without a tensor, or a tensor without heads");
-  if (a.num_tokens == 0 || (a.num_heads_q == 0 && a.num_heads_kv == 0)) return PKV_OK;
+  if (a.num_heads_q == 0 && a.num_heads_kv == 0) return PKV_OK;
   if (spec->rot_dim > 0 && !a.positions) return fail(PKV_ERR_INVALID_ARG, "positions is NULL");
   if (a.q) {
     st = validate_rows("q", a.q, a.q_stride_tok, a.q_stride_head, a.head_dim);

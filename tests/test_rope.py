@@ -91,9 +91,11 @@ def test_qk_norm_rope_refusals(pkv):
     args = pkv.make_qk_args(q=q, positions=pos)
     args.num_tokens = -1
     assert _status(pkv, lambda: pkv.qk_norm_rope(args, pkv.make_rope_spec(cos_sin=table), stream=0)) == 1
-    # nothing to do: no launch
-    args = pkv.make_qk_args(q=_Fake((0, 4, 64)), positions=_Fake((0,), "int32"))
-    pkv.qk_norm_rope(args, pkv.make_rope_spec(cos_sin=table), stream=0)
+    # nothing to do: no launch (empty tensors have no address)
+    for ptr in (0, 1 << 20):
+        args = pkv.make_qk_args(q=_Fake((0, 4, 64), ptr=ptr), k=_Fake((0, 2, 64), ptr=ptr),
+                                positions=_Fake((0,), "int32", ptr=ptr))
+        pkv.qk_norm_rope(args, pkv.make_rope_spec(cos_sin=table), stream=0)
 
 
 def test_binding_refuses_wrong_tensors(pkv):
