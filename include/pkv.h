@@ -247,7 +247,7 @@ pkv_status pkv_plan_get_stats(pkv_plan_t plan, pkv_plan_stats* stats);
 
 /* One scheduled tile as the plan made it (diagnostics and tests).  A tile over a
  * shared prefix has seq = the first of its sequences, q_row0 .. q_row0 + n_q - 1
- * rows of several of them, q_len = 1 and kv_len = the shared keys.  Rows of a
+ * rows of several of them, q_len = 1 and kv_len = kv_end.  Rows of a
  * tile are (query token, head of the tile's heads) pairs, row = token *
  * num_heads + g, query head = kv_head * G + head0 + g. */
 typedef struct {

@@ -498,7 +498,6 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
   p.status = status;
   p.cache_seqlens = args->cache_seqlens;
   p.plan_lc = reinterpret_cast<const int32_t*>(ws + plan->layout.plan_lc);
-  p.plan_min = plan->shared && plan->dynamic ? reinterpret_cast<const int32_t*>(ws + plan->layout.plan_min) : nullptr;
   p.batch = pr.batch;
   p.dynamic = plan->dynamic;
   p.row_gather = pr.page_size > 0 && pr.page_size < kBoxRows;
@@ -529,6 +528,7 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
     if (plan->dec_first) {
       // the tensor-core tiles are all over prefixes, which no append writes
       e = launch_attention(pd, tk, tv, tq, dec_ctas, pr.head_dim, fp8, false, true, append_overlaps, s);
+      p.dep_late = 1;
       if (e == cudaSuccess)
         e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, true, s);
     } else {
@@ -557,6 +557,10 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
     cp.lse = p.lse;
     cp.total_q = p.total_q;
     cp.G = p.G;
+    if (plan->shared && plan->dynamic) cp.plan_min = reinterpret_cast<const int32_t*>(ws + plan->layout.plan_min);
+    cp.cache_seqlens = p.cache_seqlens;
+    cp.batch = p.batch;
+    cp.status = p.status;
     e = plan->shared ? launch_combine_shared(cp, plan->num_combine, plan->max_combine_rows, pr.head_dim,
                                              overlap && !g_ev_stop, s)
                      : launch_combine(cp, plan->num_combine, pr.head_dim, overlap && !g_ev_stop, s);

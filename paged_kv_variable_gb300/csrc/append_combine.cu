@@ -163,6 +163,13 @@ __global__ void __launch_bounds__(kSharedCombineThreads) combine_shared_kernel(c
   const int lane = threadIdx.x & 31;
   const int rows = ci.n_q * ci.nh, parts = ci.p_nsplit + ci.nsplit;
   grid_dep_wait();  // the partials come from the attention kernel launched just before
+  if (p.plan_min != nullptr && blockIdx.x == 0 && blockIdx.y == 0) {
+    // (the attention kernel checks the lengths against their bounds)
+    for (int b = threadIdx.x; b < p.batch; b += kSharedCombineThreads) {
+      const int lc = __ldg(p.cache_seqlens + b);
+      if (lc < __ldg(p.plan_min + b)) record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
+    }
+  }
   const int row = blockIdx.y * (kSharedCombineThreads / 32) + (threadIdx.x >> 5);
   if (row < rows) {
     // partial row of part 0 of each kind, and the rows between its parts

@@ -222,7 +222,7 @@ __device__ __forceinline__ WorkItem load_item(const AttnParams& p, int it) {
   // rows placed by the caller: the sequence's query rows start where
   // cu_seqlens_q says (packed rows keep the plan's prefix sums, no load)
   if (p.q_offsets != nullptr) w.q_row0 = __ldg(p.q_offsets + w.b) + w.q_i0;
-  if (p.dynamic && !w.prefix) {  // (a shared prefix keeps its length)
+  if (p.dynamic) {
     const int bound = __ldg(p.plan_lc + w.b);
     const int lc = min(max(__ldg(p.cache_seqlens + w.b), 0), bound);
     w.lk = w.lk - bound + lc;  // the plan's key count holds bound + new tokens
@@ -246,7 +246,6 @@ __device__ __forceinline__ WorkItem q_tile(const WorkItem& w, int q, bool causal
   v.q_i0 = w.q_i0 + q * tq;
   v.q_row0 = w.q_row0 + q * tq;
   v.n_q = max(0, min(tq, w.n_q - q * tq));
-  if (w.partial >= 0) v.partial = w.partial + q * (kPrefillRowsTc / kDecodeRows);
   if (v.n_q == 0)
     v.kv_end = v.kv_begin;
   else if (causal)
@@ -424,7 +423,8 @@ __device__ void producer(const AttnParams& p, const CUtensorMap* tm_kv, const CU
   int issued = 0;
   uint32_t pi[2] = {0, 0};  // Q tiles loaded, per query tile of an item
   bool ok = true;
-  bool dep_done = false;  // waited for the append kernel (rows at or past the old cache length)
+  // waited for the append kernel (rows at or past the old cache length), or no need to
+  bool dep_done = p.dep_late != 0;
 
   for (int it = it0; it < it1 && ok; ++it) {
     const WorkItem w = load_item(p, it);
@@ -508,7 +508,7 @@ __device__ void producer(const AttnParams& p, const CUtensorMap* tm_kv, const CU
           slot = j0;
         }
       }
-      if (!dep_done && !p.dep_late && t0 + kTile > lc_old && lc_old < w.lk) {
+      if (!dep_done && t0 + kTile > lc_old && lc_old < w.lk) {
         grid_dep_wait();
         dep_done = true;
       }
@@ -556,9 +556,10 @@ __device__ void producer(const AttnParams& p, const CUtensorMap* tm_kv, const CU
     }
     __syncwarp();
   }
-  // this CTA ends only after the append kernel has: work issued after this
-  // launch on the stream then also follows the append
-  if (!dep_done) grid_dep_wait();
+  // this CTA ends only after the kernel that it overlaps (the append, or the
+  // other attention launch of the call) has: work issued after this launch on
+  // the stream then also follows that one
+  if (!dep_done || p.dep_late) grid_dep_wait();
 }
 
 // ------------------------------------------------------------------ MMA issuers (prefill tiles)
@@ -1324,9 +1325,10 @@ __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* sm
   // item's first tile (or the end of the CTA's work)
   const bool part = w.partial >= 0;
   __nv_bfloat16* dst = p.out + (int64_t)tok * p.o_stride_tok + (int64_t)head * p.o_stride_head;
-  float* pdst = p.partial_o + ((int64_t)w.partial * kDecodeRows + r) * D;
+  const int pr = qt * kPrefillRowsTc + r;  // row among the item's partial rows
+  float* pdst = p.partial_o + ((int64_t)w.partial * kDecodeRows + pr) * D;
   float* lse_dst = !valid ? nullptr
-                   : part ? p.partial_lse + (int64_t)w.partial * kDecodeRows + r
+                   : part ? p.partial_lse + (int64_t)w.partial * kDecodeRows + pr
                           : (p.lse != nullptr ? p.lse + (int64_t)head * p.total_q + tok : nullptr);
   const float lse = l > 0.f ? (part ? m + __log2f(l) : (m + __log2f(l)) * kLn2) : -INFINITY;
   if (n > 0 && part) {
@@ -1904,9 +1906,7 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
   if (blockIdx.x == 0 && mma_consumer) {
     for (int b = ctid; b < p.batch; b += 32 * L::kDecWarps) {
       const int lc = __ldg(p.cache_seqlens + b), planned = __ldg(p.plan_lc + b);
-      const int least = p.plan_min != nullptr ? __ldg(p.plan_min + b) : 0;
-      if (p.dynamic ? (lc < least || lc > planned) : lc != planned)
-        record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
+      if (p.dynamic ? (lc < 0 || lc > planned) : lc != planned) record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
     }
   }
   const float kscale = FP8 ? __ldg(p.k_scale) : 1.f;

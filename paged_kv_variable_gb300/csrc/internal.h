@@ -51,6 +51,12 @@ PKV_HOST_DEVICE inline int tc_group_heads(int G) { return G < kPrefillRowsTc ? G
 // pairs tiles only in plans without decode tiles.
 PKV_HOST_DEVICE constexpr int prefill_q_tiles(int head_dim, bool fp8) { return fp8 && head_dim <= 128 ? 2 : 1; }
 
+// lk of a tile over a shared prefix (whose rows may belong to several
+// sequences; b is the first of them): past every key, whatever the current
+// lengths, so each of its queries sees all its keys.  (A prefix is whole pages:
+// the rows of its last K/V tile past it are loaded as zeros.)
+constexpr int32_t kPrefixLk = 1 << 29;
+
 // One tile of work for one persistent CTA.  Rows of the tile are
 // (query token, head of the tile's head sub-group) pairs: row r = token * nh + g,
 // query head = hk * G + h0 + g.
@@ -69,9 +75,7 @@ struct WorkItem {
   int32_t partial;   // -1: write the final output; else the first partial slot (16 rows each)
   int32_t h0;        // first query head of the group in this tile
   int32_t nh;        // heads of the group in this tile (rows = n_q * nh)
-  int32_t prefix;    // 1: keys of a shared prefix (b: the first of its sequences; lk: its key count,
-                     // whatever the current lengths); the rows may belong to several sequences
-  int32_t pad[2];
+  int32_t pad[3];
 };
 static_assert(sizeof(WorkItem) == 64, "WorkItem layout");
 

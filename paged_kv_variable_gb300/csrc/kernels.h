@@ -62,6 +62,11 @@ struct CombineParams {
   float* lse;
   int32_t total_q;
   int32_t G;
+  // plans with shared prefixes and current lengths: [batch] least lengths to check
+  const int32_t* plan_min;  // nullable
+  const int32_t* cache_seqlens;
+  int32_t batch;
+  int* status;
 };
 
 struct AttnParams {
@@ -96,10 +101,9 @@ struct AttnParams {
   int* status;
   const int32_t* cache_seqlens;
   const int32_t* plan_lc;
-  const int32_t* plan_min;  // nullable: least cache lengths of a dynamic plan (its shared prefixes)
   int32_t batch;
   int32_t dynamic;     // plan_lc holds bounds; the cache lengths come from cache_seqlens
-  int32_t dep_late;    // the append came before the kernel this one overlaps: appended rows are there
+  int32_t dep_late;    // nothing this launch reads comes from the kernel it overlaps
 };
 
 // Start of sequence b's page list, and how many pages it has (-1: unchecked).

@@ -30,6 +30,7 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 struct Tile {
   WorkItem item;
   double cost;
+  bool prefix = false;  // over a shared prefix
 };
 
 // Groups of consecutive sequences whose first prefix_lens[g] tokens are the same.
@@ -282,6 +283,8 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
         return fail(PKV_ERR_INVALID_ARG, "group_starts must rise from 0 to at most the batch (group %d)", g);
       if (len < 0) return fail(PKV_ERR_INVALID_ARG, "negative prefix length of group %d", g);
       if (len == 0) continue;
+      if (p.cache_capacity >= kPrefixLk / 2)
+        return fail(PKV_ERR_UNSUPPORTED, "shared prefixes: cache_capacity %d is too large", p.cache_capacity);
       if (p.page_size == 0)
         return fail(PKV_ERR_UNSUPPORTED, "shared prefixes need a paged cache (a contiguous one stores a copy a sequence)");
       const int keys = len / p.page_size * p.page_size;
@@ -487,13 +490,13 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
           x.item.n_q = std::min(nt * r.tq, r.tokens - t * r.tq);
           // (each query as the one query of its row: it sees every key of the prefix)
           x.item.lq = 1;
-          x.item.lk = r.keys;
+          x.item.lk = kPrefixLk;
           x.item.kv_begin = c * r.chunk;
           x.item.kv_end = std::min(r.keys, (c + 1) * r.chunk);
           x.item.kind = r.dec ? kDecode : kPrefill;
           x.item.partial = (int32_t)num_slots;
           x.item.nh = G;  // (h0 = 0: groups of up to 64 heads)
-          x.item.prefix = 1;
+          x.prefix = true;
           const int keys = x.item.kv_end - x.item.kv_begin;
           x.cost = r.dec ? decode_cost(keys, D, esize)
                          : std::max(decode_cost(keys, D, esize), prefill_cost(keys, nt * prefill_rows, D));
@@ -695,7 +698,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   // of their CTAs an SM would spread over every SM and leave the tensor-core
   // CTAs none, and tensor-core tiles over appended keys would wait for them.
   bool tc_prefix_only = true;
-  for (const Tile& t : tiles) tc_prefix_only &= t.item.kind == kDecode || t.item.prefix != 0;
+  for (const Tile& t : tiles) tc_prefix_only &= t.item.kind == kDecode || t.prefix;
   plan->dec_first = apart && cps == 1 && tc_prefix_only;
   plan->max_combine_rows = 0;
   for (const CombineItem& c : combines) plan->max_combine_rows = std::max(plan->max_combine_rows, c.n_q * c.nh);
@@ -809,7 +812,7 @@ extern "C" pkv_status pkv_plan_get_items(pkv_plan_t plan, pkv_work_item* h_items
       o.q_index0 = w.q_i0;
       o.n_q = w.n_q;
       o.q_len = w.lq;
-      o.kv_len = w.lk;
+      o.kv_len = w.lk == kPrefixLk ? w.kv_end : w.lk;
       o.kv_begin = w.kv_begin;
       o.kv_end = w.kv_end;
       o.kind = w.kind;

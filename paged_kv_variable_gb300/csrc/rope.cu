@@ -224,7 +224,7 @@ cudaError_t launch_run(const RopeParams& p, cudaStream_t stream) {
   const int64_t tokens = std::max(p.total_q, p.a.total_new);
   const int64_t blocks = (tokens + kRopeWarps - 1) / kRopeWarps * (uq + (APPEND ? 2 : 1) * uk);
   if (blocks == 0) return cudaSuccess;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  if (blocks > INT32_MAX || tokens > INT32_MAX - kRopeWarps) return cudaErrorInvalidValue;
   rope_kernel<D, APPEND, FP8, PAIRS, HC><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }

@@ -325,6 +325,8 @@ CASES = dict(
     page1=dict(starts=[0, 20], prefix=[333], own=rnd.integers(1, 90, 20), q=[1] * 20, page=1),
     page4=dict(starts=[0, 20], prefix=[335], own=rnd.integers(1, 90, 20), q=[1] * 20, page=4),
     page4_few=dict(starts=[0, 3], prefix=[335], own=[20, 30, 8], q=[1] * 3, page=4),
+    page2=dict(starts=[0, 20], prefix=[334], own=rnd.integers(1, 90, 20), q=[1] * 20, page=2),
+    outside_split=dict(starts=[0, 10], prefix=[900], own=list(rnd.integers(1, 90, 10)) + [9000, 3, 12000], q=[1] * 13),
     page24=dict(starts=[0, 20], prefix=[480], own=rnd.integers(1, 90, 20), q=[1] * 20, page=24),
     page256=dict(starts=[0, 20], prefix=[800], own=rnd.integers(1, 900, 20), q=[1] * 20, page=256),
     ragged=dict(starts=[0, 20], prefix=[480], own=rnd.integers(1, 90, 20), q=[1] * 20, ragged=True),
@@ -334,7 +336,7 @@ CASES = dict(
     few_sms=dict(starts=[0, 20], prefix=[1900], own=rnd.integers(1, 400, 20), q=[1] * 20, num_sms=7),
 )
 FP8 = ("few_rows", "one_tile", "two_tiles", "odd_tiles", "groups", "new_tokens", "long_run_inside", "prefix_only", "d64",
-       "d256", "mqa", "wide", "page4", "page24", "many_chunks", "full", "one_sm", "few_sms")
+       "d256", "mqa", "wide", "page1", "page4", "page24", "outside_split", "many_chunks", "full", "one_sm", "few_sms")
 
 
 @pytest.mark.gpu
