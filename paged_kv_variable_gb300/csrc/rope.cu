@@ -13,9 +13,8 @@
 //
 // Bound by HBM on large calls (131072 tokens, 32 + 8 heads of 128: norm + rotation
 // 480 us = 5.74 TB/s, 84% of the measured copy bandwidth; append to an fp8 cache
-// 449 us = 6.58 TB/s, 97%), by the launch and a chain of three dependent loads
-// (sequence, length, page or table row) on a decode batch (64 tokens: 1.9 us norm +
-// rotation, 2.8 us append).
+// 442 us = 6.68 TB/s, 98%), by the launch and a chain of dependent loads (sequence,
+// page, row) on a decode batch (64 tokens: 1.9 us norm + rotation, 2.7 us append).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -45,19 +44,38 @@ __device__ __forceinline__ uint32_t codes4(const float* f, float inv) {
          ((uint32_t)f32x2_to_e4m3x2(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv)) << 16);
 }
 
-// The largest b in [0, batch) with cu[b] <= t, found by the whole warp: each
-// step probes 32 boundaries at once (two dependent loads up to 1024 sequences).
-__device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int t) {
+// Sequence and position of a token.
+struct TokenAt {
+  int b;
+  int pos;
+};
+
+// The sequence of token t (the largest b with cu[b] <= t) and its position,
+// found by the whole warp: each step probes 32 boundaries at once, and the last
+// one brings every candidate's lengths along, so nothing is loaded after the
+// search (ragged append of 2000 tokens: 14.3 -> 13.7 us, 131072 into fp8: 449 -> 442).  QUERIES:
+// the queries are the last of the positions, cache + new - queries + i.
+template <bool QUERIES>
+__device__ __forceinline__ TokenAt find_token(const RopeParams& p, int t) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, n = batch;
-  while (n > 1) {
+  const int32_t* cu = QUERIES ? p.cu_q : p.a.cu_knew;
+  int lo = 0, n = p.a.batch;
+  while (n > 32) {
     const int step = (n + 31) >> 5;
     const bool in = lane * step < n && __ldg(cu + lo + lane * step) <= t;
     const int c = max(1, __popc(__ballot_sync(0xffffffffu, in))) - 1;
     lo += c * step;
     n = min(step, n - c * step);
   }
-  return lo;
+  const int b = lo + min(lane, n - 1);
+  const int start = __ldg(cu + b);
+  int first = __ldg(p.a.cache_seqlens + b);  // the sequence's position of its token 0
+  if constexpr (QUERIES) {
+    first -= __ldg(cu + b + 1) - start;
+    if (p.a.total_new > 0) first += __ldg(p.a.cu_knew + b + 1) - __ldg(p.a.cu_knew + b);
+  }
+  const int c = max(1, __popc(__ballot_sync(0xffffffffu, lane < n && start <= t))) - 1;
+  return {lo + c, __shfl_sync(0xffffffffu, first - start, c) + t};
 }
 
 // One head's lane share: norm and rotation of the 8 values x (pieces 0..3, 4..7).
@@ -140,13 +158,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   int64_t dst = 0;
   if constexpr (APPEND) {
     if (part == 0) {
-      b = find_seq(p.cu_q, p.a.batch, t);
-      const int q0 = __ldg(p.cu_q + b), lq = __ldg(p.cu_q + b + 1) - q0;
-      const int ln = p.a.total_new > 0 ? __ldg(p.a.cu_knew + b + 1) - __ldg(p.a.cu_knew + b) : 0;
-      pos = __ldg(p.a.cache_seqlens + b) + ln - lq + (t - q0);
+      const TokenAt at = find_token<true>(p, t);
+      b = at.b;
+      pos = at.pos;
     } else {
-      b = find_seq(p.a.cu_knew, p.a.batch, t);
-      pos = __ldg(p.a.cache_seqlens + b) + (t - __ldg(p.a.cu_knew + b));
+      const TokenAt at = find_token<false>(p, t);
+      b = at.b;
+      pos = at.pos;
       if (pos < 0 || pos >= p.a.capacity) {
         if (lane == 0) record_status(p.a.status, PKV_ERR_DEVICE_BOUNDS, b, pos);
         return;
@@ -242,7 +260,10 @@ cudaError_t launch_hc(const RopeParams& p, cudaStream_t stream) {
 // at 32 + 8 heads of 128 (a call inside a captured graph): norm + rotation of 64
 // tokens 1.85 / 1.93 / 2.29 us at 1 / 2 / 4, of 512 5.30 / 4.29 / 4.67, of 4096
 // 26.9 / 20.0 / 18.0; append of 64 tokens 2.79 / 2.75 / 2.95, of 4096 34.7 /
-// 21.7 / 17.7.  8 was slower than 4 on every size but one.
+// 21.7 / 17.7.  8 was slower than 4 on every size but one.  (Not kept at 131072
+// tokens, norm + rotation / append to fp8, 480 / 449 us then: a loop over runs of heads
+// with the next run's loads ahead, 466 / 551; packed fp32 arithmetic, 492 / 443;
+// 48 registers a thread, 471 / 486.)
 template <int D, bool APPEND, bool FP8>
 cudaError_t launch_d(const RopeParams& p, cudaStream_t stream) {
   constexpr int kHeads = 256 / D;
