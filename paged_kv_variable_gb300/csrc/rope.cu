@@ -12,9 +12,9 @@
 // Everything is fp32 from the bf16 input to the one rounding at the end.
 //
 // Bound by HBM on large calls (131072 tokens, 32 + 8 heads of 128: norm + rotation
-// 480 us = 5.74 TB/s, 84% of the measured copy bandwidth; append to an fp8 cache
-// 442 us = 6.68 TB/s, 98%), by the launch and a chain of dependent loads (sequence,
-// page, row) on a decode batch (64 tokens: 1.9 us norm + rotation, 2.7 us append).
+// 393 us = 7.0 TB/s, append to an fp8 cache 414 us = 7.1 TB/s, both at the rate of
+// a plain copy), by the launch and a chain of dependent loads (sequence, page, row)
+// on a decode batch (64 tokens: 1.9 us norm + rotation, 2.6 us append).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kRopeWarps = 4;  // (8: 18.5 against 17.8 us on 4093 tokens, 469 against 449 on the 131072-token fp8 append)
 constexpr int kRopeThreads = 32 * kRopeWarps;
+constexpr int kRopeBlocks = 10;  // blocks an SM (48 registers a thread)
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -109,7 +110,7 @@ __device__ __forceinline__ void transform(float* x, bool norm, const float* w, f
 // follow from cache_seqlens; else keys go to k_out and positions are given.
 // HC: heads of a warp's run, per D / 8 lanes.
 template <int D, bool APPEND, bool FP8, bool PAIRS, int HC>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 8;          // lanes of a head
   constexpr int kHeads = 32 / kLanes;    // heads side by side in a warp
   constexpr int kRun = kHeads * HC;      // heads of a warp
@@ -132,19 +133,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int pa = (!PAIRS && rot) ? 4 * l : 8 * l;
   const int pb = (!PAIRS && rot) ? half + 4 * l : 8 * l + 4;
 
-  // the rows, all loads in flight before anything depends on one
+  // the rows, copied to shared memory while the position is looked up: a warp
+  // waiting for its position and table row holds its heads there and not in
+  // registers, so more warps fit (131072 tokens, norm + rotation: 480 -> 417 us)
   const __nv_bfloat16* src = part == 0 ? p.q + (int64_t)t * p.q_stride_tok
                                        : (part == 1 ? p.a.k_new : p.a.v_new) + (int64_t)t * p.a.n_stride_tok;
   const int64_t src_head = part == 0 ? p.q_stride_head : p.a.n_stride_head;
-  uint2 raw[HC][2];
+  __shared__ __align__(16) uint8_t rows_smem[kRopeWarps][kRun * D * 2];
+  uint8_t* mine = rows_smem[threadIdx.x >> 5];
 #pragma unroll
   for (int i = 0; i < HC; ++i) {
-    raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
-    if (h0 + i * kHeads < heads) {
-      raw[i][0] = *reinterpret_cast<const uint2*>(src + (h0 + i * kHeads) * src_head + pa);
-      raw[i][1] = *reinterpret_cast<const uint2*>(src + (h0 + i * kHeads) * src_head + pb);
-    }
+    const int h = h0 + i * kHeads;
+    if (h < heads) cp_async_16(mine + (i * kHeads + sub) * D * 2 + l * 16, src + h * src_head + l * 8, 16);
   }
+  cp_async_commit();
   float w[8];
   const __nv_bfloat16* wt = part == 0 ? p.q_weight : p.k_weight;
   const bool norm = part < 2 && wt != nullptr;
@@ -167,6 +169,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       pos = at.pos;
       if (pos < 0 || pos >= p.a.capacity) {
         if (lane == 0) record_status(p.a.status, PKV_ERR_DEVICE_BOUNDS, b, pos);
+        cp_async_wait_group<0>();  // (no copy in flight when the block ends)
         return;
       }
       if (p.a.page_size > 0) {
@@ -176,6 +179,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         const int page = (npages >= 0 && pi >= npages) ? -1 : __ldg(pages + pi);
         if (page < 0 || page >= p.a.num_pages) {
           if (lane == 0) record_status(p.a.status, PKV_ERR_DEVICE_BOUNDS, b, page);
+          cp_async_wait_group<0>();
           return;
         }
         dst = (int64_t)page * p.a.c_stride_page + (int64_t)(pos - pi * p.a.page_size) * p.a.c_stride_tok;
@@ -190,6 +194,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   // (a value row is skipped with its key row)
   if (p.rot_dim > 0 && (pos < 0 || pos >= p.num_positions)) {
     if (lane == 0) record_status(p.a.status, PKV_ERR_DEVICE_BOUNDS, b, pos);
+    cp_async_wait_group<0>();
     return;
   }
   float cs[4], sn[4];
@@ -212,13 +217,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     out = reinterpret_cast<uint8_t*>(p.q_out + (int64_t)t * p.qo_stride_tok);
     out_head = p.qo_stride_head * 2;
   }
+  cp_async_wait_group<0>();
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < HC; ++i) {
     const int h = h0 + i * kHeads;
     if (h - sub >= heads) break;  // (warp-uniform)
+    const uint8_t* in = mine + (i * kHeads + sub) * D * 2;
+    const uint2 ra = *reinterpret_cast<const uint2*>(in + 2 * pa), rb = *reinterpret_cast<const uint2*>(in + 2 * pb);
     float x[8];
-    unpack4(raw[i][0], x);
-    unpack4(raw[i][1], x + 4);
+    unpack4(ra, x);
+    unpack4(rb, x + 4);
     transform<D>(x, norm, w, p.eps, rot, PAIRS, cs, sn);  // (shuffles: every lane of the warp)
     if (h >= heads) break;
     uint8_t* row = out + h * out_head;
@@ -226,8 +235,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       *reinterpret_cast<uint32_t*>(row + pa) = codes4(x, inv);
       *reinterpret_cast<uint32_t*>(row + pb) = codes4(x + 4, inv);
     } else if (part == 2) {  // values: the bits as they came
-      *reinterpret_cast<uint2*>(row + 2 * pa) = raw[i][0];
-      *reinterpret_cast<uint2*>(row + 2 * pb) = raw[i][1];
+      *reinterpret_cast<uint2*>(row + 2 * pa) = ra;
+      *reinterpret_cast<uint2*>(row + 2 * pb) = rb;
     } else {
       *reinterpret_cast<uint2*>(row + 2 * pa) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
       *reinterpret_cast<uint2*>(row + 2 * pb) = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
@@ -253,24 +262,26 @@ cudaError_t launch_hc(const RopeParams& p, cudaStream_t stream) {
                        : launch_run<D, APPEND, FP8, false, HC>(p, stream);
 }
 
-// Heads a lane takes one after another (their loads all in flight at once): 1
-// while every warp of that split runs at once (152 SMs x 40), where a call is
-// latency; 4 from twice that on, where a warp's lookups (sequence, position,
-// table row, weights) are worth spreading over more rows; 2 between.  Measured
-// at 32 + 8 heads of 128 (a call inside a captured graph): norm + rotation of 64
-// tokens 1.85 / 1.93 / 2.29 us at 1 / 2 / 4, of 512 5.30 / 4.29 / 4.67, of 4096
-// 26.9 / 20.0 / 18.0; append of 64 tokens 2.79 / 2.75 / 2.95, of 4096 34.7 /
-// 21.7 / 17.7.  8 was slower than 4 on every size but one.  (Not kept at 131072
-// tokens, norm + rotation / append to fp8, 480 / 449 us then: a loop over runs of heads
-// with the next run's loads ahead, 466 / 551; packed fp32 arithmetic, 492 / 443;
-// 48 registers a thread, 471 / 486.)
+// Heads a lane takes one after another: 1 while every warp of that split runs at
+// once (152 SMs x 40), where a call is latency; 4 from twice that on, where a
+// warp's lookups (sequence, position, table row, weights) are worth spreading over
+// more rows; 2 between; 8 for the largest calls without an append whose heads fill
+// such runs.  Measured at 32 + 8 heads of 128 (a call inside a captured graph), us
+// at 1 / 2 / 4 / 8: norm + rotation of 64 tokens 1.91 / 2.06 / 2.31 / 3.56, of 512
+// 5.28 / 4.25 / 4.65 / 6.01, of 4096 26.6 / 18.8 / 17.1 / 18.4, of 131072 - / 507 /
+// 417 / 393; append of 64 tokens 2.57 / 2.64 / 2.77 / 2.88, of 4096 28.5 / 19.7 /
+// 17.4 / 18.1.
 template <int D, bool APPEND, bool FP8>
 cudaError_t launch_d(const RopeParams& p, cudaStream_t stream) {
   constexpr int kHeads = 256 / D;
   const int64_t warps = (int64_t)std::max(p.total_q, p.a.total_new) *
                         ((p.hq + kHeads - 1) / kHeads + (APPEND ? 2 : 1) * ((p.a.hkv + kHeads - 1) / kHeads));
   if (warps <= 6080) return launch_hc<D, APPEND, FP8, 1>(p, stream);
-  return warps < 12160 ? launch_hc<D, APPEND, FP8, 2>(p, stream) : launch_hc<D, APPEND, FP8, 4>(p, stream);
+  if (warps < 12160) return launch_hc<D, APPEND, FP8, 2>(p, stream);
+  if constexpr (!APPEND) {
+    if (warps >= 400000 && p.hq >= 8 * kHeads) return launch_hc<D, APPEND, FP8, 8>(p, stream);
+  }
+  return launch_hc<D, APPEND, FP8, 4>(p, stream);
 }
 
 }  // namespace

@@ -301,6 +301,33 @@ def test_many_rows(pkv, gpu, tokens, d, hq, hkv, interleaved):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,hq,hkv,tokens", [(64, 39, 5, 35011), (128, 21, 3, 31013), (256, 11, 1, 34001)])
+def test_a_large_call_equals_its_pieces(pkv, gpu, d, hq, hkv, tokens):
+    """The widest split of heads (eight a lane) gives the bits of the others, which smaller calls take."""
+    torch = gpu
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d)
+    x = torch.randn(tokens, hq + hkv, d, device="cuda", generator=g, dtype=torch.bfloat16)
+    pos = torch.randint(0, 500, (tokens,), device="cuda", generator=g, dtype=torch.int32)
+    table = torch.from_numpy(table64(500, d)).cuda()
+    w = (1 + 0.3 * torch.randn(d, device="cuda", generator=g)).bfloat16()
+    spec = pkv.make_rope_spec(cos_sin=table, q_weight=w, k_weight=w)
+    outs = [torch.zeros_like(x) for _ in range(2)]
+
+    def call(out, a, b):
+        pkv.qk_norm_rope(pkv.make_qk_args(q=x[a:b, :hq], k=x[a:b, hq:], positions=pos[a:b], q_out=out[a:b, :hq],
+                                          k_out=out[a:b, hq:]), spec)
+
+    call(outs[0], 0, tokens)
+    for a in range(0, tokens, 5000):
+        call(outs[1], a, min(tokens, a + 5000))
+    assert torch.equal(*outs)
+    n = 64
+    want, mag = rows64(np64(x[-n:]), np64(w), pos[-n:].cpu().numpy(), table.cpu().numpy(), False, 1e-6)
+    close_bf16(outs[0][-n:], want, mag)
+
+
+@pytest.mark.gpu
 def test_qk_norm_rope_one_side_and_strides(pkv, gpu):
     """q alone, k alone, heads outermost, another stream."""
     torch = gpu
