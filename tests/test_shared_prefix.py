@@ -336,7 +336,7 @@ CASES = dict(
     few_sms=dict(starts=[0, 20], prefix=[1900], own=rnd.integers(1, 400, 20), q=[1] * 20, num_sms=7),
 )
 FP8 = ("few_rows", "one_tile", "two_tiles", "odd_tiles", "groups", "new_tokens", "long_run_inside", "prefix_only", "d64",
-       "d256", "mqa", "wide", "page1", "page4", "page24", "outside_split", "many_chunks", "full", "one_sm", "few_sms")
+       "d256", "d256_few", "page2", "mqa", "wide", "page1", "page4", "page24", "outside_split", "many_chunks", "full", "one_sm", "few_sms")
 
 
 @pytest.mark.gpu
@@ -384,6 +384,46 @@ def test_same_bits_every_run_and_near_the_plain_plan(pkv, gpu, name):
     pkv.attn_varlen_kvcache_fwd_noalloc(c.problem, c.args(), c.plan)
     assert pkv.get_status_noalloc() == 0
     assert torch.equal(first, c.out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["two_tiles", "few_rows", "d64", "d256"])
+def test_strided_queries_and_outputs(pkv, gpu, name):
+    """Queries out of a packed projection, outputs into wider rows, no lse; nothing around them is written."""
+    torch = gpu
+    c = Shared(pkv, torch, 13, **CASES[name])
+    tq, hq, d = c.q.shape
+    packed = torch.full((tq + 2, hq + 3, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    packed[:tq, 1:hq + 1] = c.q
+    c.q = packed[:tq, 1:hq + 1]
+    wide = torch.full((tq + 2, hq, d + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.out = wide[1:tq + 1, :, :d]
+    assert c.run() == 0
+    c.check()
+    first = c.out.clone()
+    assert torch.all(wide[0] == 7.0) and torch.all(wide[tq + 1] == 7.0) and torch.all(wide[:, :, d:] == 7.0)
+    c.out.fill_(0.0)
+    pkv.attn_varlen_kvcache_fwd(c.problem, c.args(lse=None), c.plan, c.ws)
+    assert pkv.get_status(c.ws) == 0
+    assert torch.equal(first, c.out)
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(pkv, gpu):
+    """Calls on two streams, each with its plan and workspace."""
+    torch = gpu
+    cases = [Shared(pkv, torch, 14, **CASES["full"]), Shared(pkv, torch, 15, fp8=True, **CASES["two_tiles"]),
+             Shared(pkv, torch, 16, **CASES["new_tokens"])]
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [c.args() for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, a, st in zip(cases, args, streams):
+            pkv.attn_varlen_kvcache_fwd(c.problem, a, c.plan, c.ws, stream=st)
+    torch.cuda.synchronize()
+    for c in cases:
+        assert pkv.get_status(c.ws) == 0
+        c.check()
 
 
 @pytest.mark.gpu
