@@ -1275,7 +1275,15 @@ __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* sm
 
     const bool zero_v = !FP8 && (!L::kQQ || zero_owner) && t0 + kTile > w.lk;
     if (zero_v) {
-      // rows past the sequence may hold anything (even NaN): zero them in V
+      // rows past the sequence may hold anything (even NaN): zero them in V.
+      // The softmax runs up to kSBufs tiles ahead of P V; with fewer V stages
+      // (D = 256) the stage may still wait for its previous tile, whose
+      // unfinished phase would pass for this one's: that tile's P V first.
+      if constexpr (!L::kQQ && L::kStagesV < L::kSBufs) {
+        if (T >= (uint32_t)L::kStagesV &&
+            !warp_wait(&B.o_done[(T - L::kStagesV) % L::kSBufs], ((T - L::kStagesV) / L::kSBufs) & 1, abort_flag))
+          return false;
+      }
       if (!warp_wait(&B.full_v[rv.stage], rv.phase, abort_flag)) return false;
       if (r < kTile && t0 + r >= w.lk) {
         uint8_t* vrow = smem + L::kVOff + rv.stage * L::kTileBytes + r * 128;

@@ -387,6 +387,19 @@ def test_same_bits_every_run_and_near_the_plain_plan(pkv, gpu, name):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("page", [1, 4, 16])
+def test_long_query_runs_of_one_cta_at_head_dim_256(pkv, gpu, page):
+    """Items one after another on one SM, whose last V tile has rows past the sequence to zero: the zeros go into
+    that tile's stage, not into the one before it that still waits for its copies (slow over small pages)."""
+    c = Shared(pkv, gpu, 7, starts=[0, 8], prefix=[0], own=[1255] * 8, q=[33] * 8, hq=24, hkv=3, d=256, page=page,
+               num_sms=1, shares=False)
+    for _ in range(3):
+        c.out.fill_(float("nan"))
+        assert c.run() == 0
+        c.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("name", ["two_tiles", "few_rows", "d64", "d256"])
 def test_strided_queries_and_outputs(pkv, gpu, name):
     """Queries out of a packed projection, outputs into wider rows, no lse; nothing around them is written."""
