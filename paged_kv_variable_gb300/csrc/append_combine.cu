@@ -152,7 +152,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
 // over the sequence's own keys.  One warp per row: each lane takes the LSE of
 // one part (the common max and the weights come from the warp's lanes), then
 // D / 32 columns of every part's row.  Parts are added in a fixed order, the
-// prefix's first.
+// prefix's first.  Latency alone bounds it (2048 rows of two parts: 4% of the
+// DRAM bandwidth): a warp a row keeps the chain at item, parts, output (a block
+// a unit, its rows one after another, took 24 us on 3072 rows of a wide group).
 constexpr int kSharedCombineThreads = 128;
 
 template <int D>
@@ -184,6 +186,25 @@ __global__ void __launch_bounds__(kSharedCombineThreads) combine_shared_kernel(c
       return s < ci.p_nsplit ? prow + (int64_t)s * ci.p_chunk_slots * kDecodeRows
                              : orow + (int64_t)(s - ci.p_nsplit) * ci.slot_stride * kDecodeRows;
     };
+    auto load = [&](int s, float* v) {
+      const float* src = p.partial_o + part_row(s) * D + lane * E;
+      if constexpr (E == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] = x.x, v[1] = x.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src + i);
+          v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+        }
+      }
+    };
+    // the first parts' rows are in flight while the weights are made
+    constexpr int kAhead = 4;
+    float ahead[kAhead][E];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+      if (s < parts) load(s, ahead[s]);
     float m = -INFINITY;
     for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.partial_lse[part_row(s)]);
 #pragma unroll
@@ -197,24 +218,24 @@ __global__ void __launch_bounds__(kSharedCombineThreads) combine_shared_kernel(c
       const int n = min(32, parts - s0);
       const float w = lane < n ? ex2(p.partial_lse[part_row(s0 + lane)] - mu) : 0.f;
       wsum += w;
-#pragma unroll 4
-      for (int s = 0; s < n; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, w, s);
-        const float* src = p.partial_o + part_row(s0 + s) * D + lane * E;
-        if constexpr (E == 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          acc[0] = fmaf(ws, v.x, acc[0]);
-          acc[1] = fmaf(ws, v.y, acc[1]);
-        } else {
+      int s = 0;
+      if (s0 == 0) {
 #pragma unroll
-          for (int i = 0; i < E; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src + i);
-            acc[i] = fmaf(ws, v.x, acc[i]);
-            acc[i + 1] = fmaf(ws, v.y, acc[i + 1]);
-            acc[i + 2] = fmaf(ws, v.z, acc[i + 2]);
-            acc[i + 3] = fmaf(ws, v.w, acc[i + 3]);
+        for (; s < kAhead; ++s) {
+          const float ws = __shfl_sync(0xffffffffu, w, s);
+          if (s < n) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = fmaf(ws, ahead[s][i], acc[i]);
           }
         }
+      }
+#pragma unroll 4
+      for (; s < n; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        float v[E];
+        load(s0 + s, v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = fmaf(ws, v[i], acc[i]);
       }
     }
 #pragma unroll
