@@ -517,6 +517,13 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
   const bool overlap = plan->num_prefill_items == 0;
   const bool fp8 = pr.cache_dtype == PKV_FP8_E4M3;
   const bool append_overlaps = plan->total_new > 0 && !rope && !g_ev_start;
+  // A call without an append starts while the stream's previous kernel drains
+  // and waits for it before it reads anything (decode-only plans and those with
+  // shared prefixes, where the instance can).
+  const bool first_pf = plan->num_ctas_tc > 0 ? !plan->dec_first : plan->num_prefill_items > 0;
+  const bool first = plan->total_new == 0 && !rope && !g_ev_start && (overlap || plan->shared) &&
+                     starts_early(pr.head_dim, fp8, first_pf);
+  p.dep_first = first;
   if (plan->num_ctas_tc > 0) {
     // A plan with shared prefixes and both kinds of tiles: the tensor-core tiles
     // on num_ctas_tc SMs and the decode tiles on the others, each in the
@@ -527,20 +534,22 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
     const int dec_ctas = plan->num_ctas - plan->num_ctas_tc;
     if (plan->dec_first) {
       // the tensor-core tiles are all over prefixes, which no append writes
-      e = launch_attention(pd, tk, tv, tq, dec_ctas, pr.head_dim, fp8, false, true, append_overlaps, s);
+      e = launch_attention(pd, tk, tv, tq, dec_ctas, pr.head_dim, fp8, false, true, append_overlaps || first, s);
+      p.dep_first = 0;
       p.dep_late = 1;
       if (e == cudaSuccess)
         e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, true, s);
     } else {
       // the append is complete before the first launch starts
-      e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, false, s);
+      e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, first, s);
+      pd.dep_first = 0;
       pd.dep_late = 1;
       if (e == cudaSuccess)
         e = launch_attention(pd, tk, tv, tq, dec_ctas, pr.head_dim, fp8, false, true, true, s);
     }
   } else {
     e = launch_attention(p, tk, tv, tq, plan->num_ctas, pr.head_dim, fp8, plan->num_prefill_items > 0,
-                         plan->num_decode_items > 0, overlap && append_overlaps, s);
+                         plan->num_decode_items > 0, (overlap && append_overlaps) || first, s);
   }
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   if (g_ev_stop && (e = record_profile_event(g_ev_stop, s)) != cudaSuccess) return cuda_fail(e, "profile event");

@@ -2069,6 +2069,9 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = L::kTc ? *tmem_slot : 0u;
+  if constexpr (starts_early(D, FP8, PF)) {
+    if (p.dep_first) grid_dep_wait();
+  }
   grid_dep_launch();  // the combine kernel may be scheduled; it waits for this grid to finish
   const int it0 = p.cta_begin[blockIdx.x], it1 = p.cta_begin[blockIdx.x + 1];
   if constexpr (L::kSplitRegs) {

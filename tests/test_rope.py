@@ -528,6 +528,49 @@ def test_rope_kv_append_equals_the_steps_apart(pkv, gpu, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [3, 900])
+def test_calls_between_kernels_that_write_and_read(pkv, gpu, tokens):
+    """A call may start while the kernel before it drains: it reads what that kernel wrote (queries, keys, lengths),
+    and what follows reads its results, from the host and in a graph."""
+    torch = gpu
+    c = AppendCase(pkv, torch, 30, d=128, page=16, fp8=False, new=[tokens, 1, tokens], cached=[3, 40, 9], norm="qk",
+                   far=tokens + 64)
+    inputs = [(bf16(torch, np.random.default_rng(i), *c.q.shape), H.i32(c.cached - i)) for i in range(3)]
+    pos = H.i32(c.positions()[0])
+    qk = pkv.make_qk_args(q=c.q_out, positions=pos)
+    args, total = c.args(), torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+    busy = torch.randn(1 << 24, device="cuda")
+
+    def step(i, got):
+        busy.mul_(1.0001)
+        c.q.copy_(inputs[i % 3][0])
+        c.lens.copy_(inputs[i % 3][1])
+        pkv.rope_kv_append(c.problem, args, c.rope, c.tq, c.tn)
+        pkv.qk_norm_rope(qk, c.spec)               # once more over its own queries, in place
+        got.copy_(c.q_out)
+
+    want = []
+    for i in range(3):
+        step(i, total)
+        torch.cuda.synchronize()
+        want.append((total.clone(), c.kc.clone()))
+    got = [torch.empty_like(total) for _ in range(12)]
+    for i, g in enumerate(got):
+        step(i, g)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 3][0]) for i, g in enumerate(got))
+    for g in got:
+        g.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i, g in enumerate(got):
+            step(i, g)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 3][0]) for i, g in enumerate(got))
+
+
+@pytest.mark.gpu
 def test_rope_kv_append_in_place_and_twice(pkv, gpu):
     """Queries rotated in place; two calls of one batch write the same."""
     torch = gpu

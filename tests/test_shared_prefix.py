@@ -422,6 +422,73 @@ def test_strided_queries_and_outputs(pkv, gpu, name):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,fp8", [("two_tiles", False), ("two_tiles", True), ("few_rows", False), ("d64", False),
+                                      ("mqa", True), ("not_shared", False), ("d256", False)])
+def test_calls_between_kernels_that_write_and_read(pkv, gpu, name, fp8):
+    """A call may start while the kernel before it drains: it attends the queries which that kernel wrote, and what
+    follows reads its output, call after call, from the host and in a graph."""
+    torch = gpu
+    c = Shared(pkv, torch, 17, fp8=fp8, **CASES[name])
+    queries = [c.q.clone(), (c.q.float() * 0.5 + 0.1).bfloat16(), c.q.flip(0).contiguous()]
+    want = []
+    for q in queries:
+        c.q.copy_(q)
+        torch.cuda.synchronize()
+        assert c.run() == 0
+        torch.cuda.synchronize()
+        want.append(c.out.clone())
+    busy = torch.randn(1 << 24, device="cuda")
+    args = c.args()
+
+    def chain(got):
+        for i in range(12):
+            busy.mul_(1.0001)                     # something that takes a while
+            c.q.copy_(queries[i % 3])
+            pkv.attn_varlen_kvcache_fwd(c.problem, args, c.plan, c.ws)
+            got[i].copy_(c.out)
+
+    got = [torch.empty_like(c.out) for _ in range(12)]
+    chain(got)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
+    for g in got:
+        g.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(got)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
+    assert pkv.get_status(c.ws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["two_tiles", "few_rows"])
+def test_queries_from_another_stream(pkv, gpu, name):
+    """The queries come from a side stream, joined by an event right before the call."""
+    torch = gpu
+    c = Shared(pkv, torch, 18, **CASES[name])
+    assert c.run() == 0
+    want, q = c.out.clone(), c.q.clone()
+    busy, side, args = torch.randn(1 << 25, device="cuda"), torch.cuda.Stream(), c.args()
+    main = torch.cuda.current_stream()
+    for _ in range(5):
+        c.q.fill_(0.0)
+        c.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            busy.mul_(1.0001)
+            c.q.copy_(q)
+        c.lens.add_(0)                            # a kernel of the call's own stream, done at once
+        main.wait_stream(side)
+        pkv.attn_varlen_kvcache_fwd(c.problem, args, c.plan, c.ws)
+        torch.cuda.synchronize()
+        assert torch.equal(want, c.out)
+    assert pkv.get_status(c.ws) == 0
+
+
+@pytest.mark.gpu
 def test_two_calls_at_once(pkv, gpu):
     """Calls on two streams, each with its plan and workspace."""
     torch = gpu
