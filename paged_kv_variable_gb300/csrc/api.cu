@@ -512,16 +512,16 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
   // append kernel and the combine kernel's start with the attention's end.
   // Plans with prefill tiles keep the kernels strictly in order: there the
   // overlap measured slower (large appends, long attention kernels).  Never
-  // across a profiling event, which must see the kernels in order, nor over a
-  // rotating append, whose queries the attention reads from its start.
+  // across a profiling event, which must see the kernels in order.
   const bool overlap = plan->num_prefill_items == 0;
   const bool fp8 = pr.cache_dtype == PKV_FP8_E4M3;
   const bool append_overlaps = plan->total_new > 0 && !rope && !g_ev_start;
-  // A call without an append starts while the stream's previous kernel drains
-  // and waits for it before it reads anything (decode-only plans and those with
+  // Without an append, or after the rotating one (whose queries it reads from its
+  // start), the attention starts while the stream's previous kernel drains and
+  // waits for it before it reads anything (decode-only plans and those with
   // shared prefixes, where the instance can).
   const bool first_pf = plan->num_ctas_tc > 0 ? !plan->dec_first : plan->num_prefill_items > 0;
-  const bool first = plan->total_new == 0 && !rope && !g_ev_start && (overlap || plan->shared) &&
+  const bool first = (plan->total_new == 0 || rope) && !g_ev_start && (overlap || plan->shared) &&
                      starts_early(pr.head_dim, fp8, first_pf);
   p.dep_first = first;
   if (plan->num_ctas_tc > 0) {
