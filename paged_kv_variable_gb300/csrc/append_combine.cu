@@ -305,7 +305,8 @@ cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int max
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)num_items, (unsigned)((max_rows + kSharedCombineThreads / 32 - 1) / (kSharedCombineThreads / 32)));
+  constexpr int kWarps = kSharedCombineThreads / 32;
+  cfg.gridDim = dim3((unsigned)num_items, (unsigned)((max_rows + kWarps - 1) / kWarps));
   cfg.blockDim = dim3((unsigned)kSharedCombineThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = stream;

@@ -286,7 +286,8 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
       if (p.cache_capacity >= kPrefixLk / 2)
         return fail(PKV_ERR_UNSUPPORTED, "shared prefixes: cache_capacity %d is too large", p.cache_capacity);
       if (p.page_size == 0)
-        return fail(PKV_ERR_UNSUPPORTED, "shared prefixes need a paged cache (a contiguous one stores a copy a sequence)");
+        return fail(PKV_ERR_UNSUPPORTED,
+                    "shared prefixes need a paged cache (a contiguous one stores a copy a sequence)");
       const int keys = len / p.page_size * p.page_size;
       PrefixRun run{};
       int members = 0;
@@ -757,7 +758,8 @@ pkv_status make_plan_noexcept(Args... args) noexcept {
 extern "C" pkv_status pkv_plan(const pkv_problem* problem, const int32_t* h_q_lens,
                                const int32_t* h_cache_lens, const int32_t* h_new_lens,
                                int32_t num_sms, pkv_plan_t* out_plan, size_t* out_workspace_bytes) {
-  return make_plan_noexcept(problem, h_q_lens, h_cache_lens, h_new_lens, num_sms, false, nullptr, out_plan, out_workspace_bytes);
+  return make_plan_noexcept(problem, h_q_lens, h_cache_lens, h_new_lens, num_sms, false, nullptr, out_plan,
+                            out_workspace_bytes);
 }
 
 extern "C" pkv_status pkv_plan_decode_dynamic(const pkv_problem* problem, const int32_t* h_q_lens,
