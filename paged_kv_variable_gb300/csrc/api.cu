@@ -570,9 +570,10 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
     cp.cache_seqlens = p.cache_seqlens;
     cp.batch = p.batch;
     cp.status = p.status;
-    e = plan->shared ? launch_combine_shared(cp, plan->num_combine, plan->max_combine_rows, pr.head_dim,
-                                             overlap && !g_ev_stop, s)
-                     : launch_combine(cp, plan->num_combine, pr.head_dim, overlap && !g_ev_stop, s);
+    e = plan->row_combine
+            ? launch_combine_shared(cp, plan->num_combine, plan->max_combine_rows, plan->max_combine_parts, pr.head_dim,
+                                    overlap && !g_ev_stop, s)
+            : launch_combine(cp, plan->num_combine, pr.head_dim, overlap && !g_ev_stop, s);
     if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   }
   return PKV_OK;

@@ -147,115 +147,131 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
   }
 }
 
-// The merge for plans with shared prefixes: a unit's rows have parts over the
-// chunks of the prefix, in the tiles of the sequences that share it, and parts
-// over the sequence's own keys.  One warp per row: each lane takes the LSE of
+// The merge for plans of pkv_plan_shared_prefix: a unit's rows may have parts over
+// the chunks of a prefix, in the tiles of the sequences that share it, besides
+// the parts over the sequence's own keys.  One warp per row: each lane takes the LSE of
 // one part (the common max and the weights come from the warp's lanes), then
 // D / 32 columns of every part's row.  Parts are added in a fixed order, the
 // prefix's first.  Latency alone bounds it (2048 rows of two parts: 4% of the
 // DRAM bandwidth): a warp a row keeps the chain at item, parts, output (a block
 // a unit, its rows one after another, took 24 us on 3072 rows of a wide group).
-constexpr int kSharedCombineThreads = 128;
+constexpr int kSharedCombineWarps = 4;
 
-template <int D>
-__global__ void __launch_bounds__(kSharedCombineThreads) combine_shared_kernel(const CombineParams p) {
+// SPLIT: a block takes one row, its warps every fourth part each (rows of many
+// parts, which are few; their sums are joined in a fixed order); else a warp a
+// row.
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(32 * kSharedCombineWarps) combine_shared_kernel(const CombineParams p) {
   constexpr int E = D / 32;  // columns of a lane: 8, 4 or 2
+  constexpr int W = SPLIT ? kSharedCombineWarps : 1;
   constexpr float kLn2 = 0.693147180559945309f;
   const CombineItem ci = p.items[blockIdx.x];
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = ci.n_q * ci.nh, parts = ci.p_nsplit + ci.nsplit;
   grid_dep_wait();  // the partials come from the attention kernel launched just before
   if (p.plan_min != nullptr && blockIdx.x == 0 && blockIdx.y == 0) {
     // (the attention kernel checks the lengths against their bounds)
-    for (int b = threadIdx.x; b < p.batch; b += kSharedCombineThreads) {
+    for (int b = threadIdx.x; b < p.batch; b += 32 * kSharedCombineWarps) {
       const int lc = __ldg(p.cache_seqlens + b);
       if (lc < __ldg(p.plan_min + b)) record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
     }
   }
-  const int row = blockIdx.y * (kSharedCombineThreads / 32) + (threadIdx.x >> 5);
-  if (row < rows) {
-    // partial row of part 0 of each kind, and the rows between its parts
-    const int tok = row / ci.nh, g = row - tok * ci.nh;
-    const int pt = ci.p_tok0 + tok;
-    const int64_t prow =
-        ci.p_nsplit == 0 ? 0
-                         : ((int64_t)ci.p_slot0 + (int64_t)(pt / ci.p_tq) * ci.p_tile_slots) * kDecodeRows +
-                               (pt % ci.p_tq) * ci.nh + g;
-    const int64_t orow = (int64_t)ci.slot0 * kDecodeRows + row;
-    auto part_row = [&](int s) {
-      return s < ci.p_nsplit ? prow + (int64_t)s * ci.p_chunk_slots * kDecodeRows
-                             : orow + (int64_t)(s - ci.p_nsplit) * ci.slot_stride * kDecodeRows;
-    };
-    auto load = [&](int s, float* v) {
-      const float* src = p.partial_o + part_row(s) * D + lane * E;
-      if constexpr (E == 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        v[0] = x.x, v[1] = x.y;
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; i += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src + i);
-          v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-        }
-      }
-    };
-    // the first parts' rows are in flight while the weights are made
-    constexpr int kAhead = 4;
-    float ahead[kAhead][E];
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s)
-      if (s < parts) load(s, ahead[s]);
-    float m = -INFINITY;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.partial_lse[part_row(s)]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float mu = m == -INFINITY ? 0.f : m;
-    float wsum = 0.f;
-    float acc[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = 0.f;
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-      const int n = min(32, parts - s0);
-      const float w = lane < n ? ex2(p.partial_lse[part_row(s0 + lane)] - mu) : 0.f;
-      wsum += w;
-      int s = 0;
-      if (s0 == 0) {
-#pragma unroll
-        for (; s < kAhead; ++s) {
-          const float ws = __shfl_sync(0xffffffffu, w, s);
-          if (s < n) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = fmaf(ws, ahead[s][i], acc[i]);
-          }
-        }
-      }
-#pragma unroll 4
-      for (; s < n; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, w, s);
-        float v[E];
-        load(s0 + s, v);
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = fmaf(ws, v[i], acc[i]);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-    const int out_row = ci.q_row0 + tok, head = ci.hk * p.G + ci.h0 + g;
-    __nv_bfloat16* dst = p.out + (int64_t)out_row * p.o_stride_tok + (int64_t)head * p.o_stride_head + lane * E;
+  const int row = SPLIT ? (int)blockIdx.y : blockIdx.y * kSharedCombineWarps + warp;
+  if (row >= rows) return;  // (SPLIT: the whole block)
+  const int w0 = SPLIT ? warp : 0;  // this warp's parts: w0, w0 + W, ...
+  // partial row of part 0 of each kind, and the rows between its parts
+  const int tok = row / ci.nh, g = row - tok * ci.nh;
+  const int pt = ci.p_tok0 + tok;
+  const int64_t prow = ci.p_nsplit == 0
+                           ? 0
+                           : ((int64_t)ci.p_slot0 + (int64_t)(pt / ci.p_tq) * ci.p_tile_slots) * kDecodeRows +
+                                 (pt % ci.p_tq) * ci.nh + g;
+  const int64_t orow = (int64_t)ci.slot0 * kDecodeRows + row;
+  auto part_row = [&](int s) {
+    return s < ci.p_nsplit ? prow + (int64_t)s * ci.p_chunk_slots * kDecodeRows
+                           : orow + (int64_t)(s - ci.p_nsplit) * ci.slot_stride * kDecodeRows;
+  };
+  auto load = [&](int s, float* v) {
+    const float* src = p.partial_o + part_row(s) * D + lane * E;
     if constexpr (E == 2) {
-      *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    } else if constexpr (E == 4) {
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      v[0] = x.x, v[1] = x.y;
     } else {
-      *reinterpret_cast<uint4*>(dst) =
-          make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
-                     pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
+#pragma unroll
+      for (int i = 0; i < E; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src + i);
+        v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+      }
     }
-    if (p.lse != nullptr && lane == 0)
-      p.lse[(int64_t)head * p.total_q + out_row] = wsum > 0.f ? (mu + __log2f(wsum)) * kLn2 : -INFINITY;
+  };
+  // the first parts' rows are in flight while the weights are made
+  constexpr int kAhead = 4;
+  float ahead[kAhead][E];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (w0 + k * W < parts) load(w0 + k * W, ahead[k]);
+  float m = -INFINITY;
+  for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.partial_lse[part_row(s)]);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float mu = m == -INFINITY ? 0.f : m;
+  float wsum = 0.f;
+  float acc[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0.f;
+  for (int s0 = 0; s0 < parts; s0 += 32) {
+    const int n = min(32, parts - s0);
+    const float w = lane < n ? ex2(p.partial_lse[part_row(s0 + lane)] - mu) : 0.f;
+    wsum += w;
+    int s = w0;
+    if (s0 == 0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k, s += W) {
+        const float ws = __shfl_sync(0xffffffffu, w, s & 31);
+        if (s < n) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc[i] = fmaf(ws, ahead[k][i], acc[i]);
+        }
+      }
+    }
+#pragma unroll 4
+    for (; s < n; s += W) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      float v[E];
+      load(s0 + s, v);
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] = fmaf(ws, v[i], acc[i]);
+    }
   }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+  if constexpr (SPLIT) {
+    __shared__ float sums[W][D];
+#pragma unroll
+    for (int i = 0; i < E; ++i) sums[warp][lane * E + i] = acc[i];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int k = 1; k < W; ++k)
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] += sums[k][lane * E + i];
+  }
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const int out_row = (p.q_offsets != nullptr ? __ldg(p.q_offsets + ci.b) : ci.q_row0) + tok;
+  const int head = ci.hk * p.G + ci.h0 + g;
+  __nv_bfloat16* dst = p.out + (int64_t)out_row * p.o_stride_tok + (int64_t)head * p.o_stride_head + lane * E;
+  if constexpr (E == 2) {
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+  } else if constexpr (E == 4) {
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+  } else {
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
+                   pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
+  }
+  if (p.lse != nullptr && lane == 0)
+    p.lse[(int64_t)head * p.total_q + out_row] = wsum > 0.f ? (mu + __log2f(wsum)) * kLn2 : -INFINITY;
 }
 
 cudaError_t launch_kv_append(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream) {
@@ -298,23 +314,28 @@ cudaError_t launch_combine(const CombineParams& p, int num_items, int head_dim, 
                            : cudaLaunchKernelEx(&cfg, combine_kernel<64>, p);
 }
 
-cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int max_rows, int head_dim,
+cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int max_rows, int max_parts, int head_dim,
                                   bool overlap_prev, cudaStream_t stream) {
   if (num_items == 0) return cudaSuccess;
+  const bool split = max_parts > 8;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  constexpr int kWarps = kSharedCombineThreads / 32;
-  cfg.gridDim = dim3((unsigned)num_items, (unsigned)((max_rows + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3((unsigned)kSharedCombineThreads);
+  cfg.gridDim = dim3((unsigned)num_items,
+                     (unsigned)(split ? max_rows : (max_rows + kSharedCombineWarps - 1) / kSharedCombineWarps));
+  cfg.blockDim = dim3(32u * kSharedCombineWarps);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = overlap_prev ? 1 : 0;
-  return head_dim == 256   ? cudaLaunchKernelEx(&cfg, combine_shared_kernel<256>, p)
-         : head_dim == 128 ? cudaLaunchKernelEx(&cfg, combine_shared_kernel<128>, p)
-                           : cudaLaunchKernelEx(&cfg, combine_shared_kernel<64>, p);
+  if (split)
+    return head_dim == 256   ? cudaLaunchKernelEx(&cfg, combine_shared_kernel<256, true>, p)
+           : head_dim == 128 ? cudaLaunchKernelEx(&cfg, combine_shared_kernel<128, true>, p)
+                             : cudaLaunchKernelEx(&cfg, combine_shared_kernel<64, true>, p);
+  return head_dim == 256   ? cudaLaunchKernelEx(&cfg, combine_shared_kernel<256, false>, p)
+         : head_dim == 128 ? cudaLaunchKernelEx(&cfg, combine_shared_kernel<128, false>, p)
+                           : cudaLaunchKernelEx(&cfg, combine_shared_kernel<64, false>, p);
 }
 
 }  // namespace pkv

@@ -127,7 +127,8 @@ struct pkv_plan_s {
   int32_t num_ctas;
   int32_t num_ctas_tc;  // > 0: the first of them run tensor-core tiles, in a launch of their own
   int32_t dec_first;    // the decode tiles' launch comes first
-  int32_t max_combine_rows;  // rows of the largest split unit
+  int32_t max_combine_rows;   // rows of the largest split unit
+  int32_t max_combine_parts;  // parts of the unit with most
   int32_t num_slots;
   int32_t total_q;
   int32_t total_new;
@@ -142,6 +143,7 @@ struct pkv_plan_s {
   int32_t num_combine;
   int32_t dynamic;  // cache lengths read on the device; plan_lc holds their bounds
   int32_t shared;   // some prefix is computed once for several sequences
+  int32_t row_combine;  // made by pkv_plan_shared_prefix: merged a warp (or block) a row
   double* item_cost;  // [num_items] model cost of each item, in work-list order
 };
 

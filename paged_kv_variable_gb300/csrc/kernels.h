@@ -128,9 +128,9 @@ cudaError_t launch_rope_kv_append(const RopeParams& p, int head_dim, bool fp8, c
 // the kernel waits for that one before reading what it wrote.
 cudaError_t launch_combine(const CombineParams& p, int num_items, int head_dim, bool overlap_prev,
                            cudaStream_t stream);
-// the same for plans with shared prefixes (parts over the prefix and over each sequence's own keys)
-cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int max_rows, int head_dim,
-                                  bool overlap_prev, cudaStream_t stream);
+// the same for plans made for shared prefixes (parts over the prefix and over each sequence's own keys)
+cudaError_t launch_combine_shared(const CombineParams& p, int num_items, int max_rows, int max_parts,
+                                  int head_dim, bool overlap_prev, cudaStream_t stream);
 cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const CUtensorMap& tm_q, int num_ctas, int head_dim, bool fp8, bool has_prefill,
                              bool has_decode, bool overlap_prev, cudaStream_t stream);

@@ -68,37 +68,47 @@ double prefill_cost(int keys, int rows, int d) { return 256.0 + keys * (rows * d
 // measurements on a GB300: what the choice of SMs and chunks below balances.
 struct TimeModel {
   double tile1, tile2;  // a tensor-core K/V tile of 128 keys, one and two query tiles
-  double sm_rate, hbm;  // decode tiles: bytes a us of one SM and of all
-  int cps;              // decode CTAs an SM
+  // a decode CTA: bytes a us, us an item besides, least us an item; the GPU's bytes a us
+  double rate, item, least, hbm;
+  int cps;  // decode CTAs an SM
+  int d;
   double key_bytes;
-  TimeModel(int d, bool fp8) {
+  TimeModel(int head_dim, bool fp8) : d(head_dim) {
     if (fp8) {
       tile1 = d == 64 ? 2.0 : d == 128 ? 3.0 : 4.0;
       tile2 = d == 64 ? 2.6 : 3.8;
-      sm_rate = d == 64 ? 20e3 : d == 128 ? 31e3 : 25e3;
-      hbm = sm_rate * 152;
+      rate = d == 64 ? 19e3 : d == 128 ? 28e3 : 43e3;
+      item = d == 64 ? 1.4 : 3.0;
+      least = d == 64 ? 2.3 : 3.7;
+      hbm = d == 64 ? 4.6e6 : 5.4e6;
     } else {
       tile1 = tile2 = d == 64 ? 1.0 : d == 128 ? 1.1 : 2.2;
-      sm_rate = d == 64 ? 38e3 : 54e3;
-      hbm = d == 64 ? 5.4e6 : 6.1e6;
+      rate = d == 64 ? 26e3 : d == 128 ? 57e3 : 49e3;
+      item = d == 64 ? 1.0 : d == 128 ? 1.2 : 0.6;
+      least = d == 64 ? 2.4 : d == 128 ? 2.8 : 3.5;
+      hbm = 6.3e6;
     }
     cps = (fp8 ? d <= 128 : d == 64) ? 2 : 1;
     key_bytes = 2.0 * d * (fp8 ? 1 : 2);
   }
-  static constexpr double kItemTc = 4.5;   // start and end of a tensor-core chunk
-  static constexpr double kItemDec = 1.2;  // of a decode item
-  static constexpr double kParts = 4.0;    // the combine kernel
-  static constexpr double kPartRate = 5e6;  // bytes a us of partials written and read
+  static constexpr double kItemTc = 4.5;    // start and end of a tensor-core chunk
 
   // `keys` of decode work in `units` units, the longest of `longest` keys
   double decode(int64_t keys, int64_t units, int64_t longest, int sms) const {
-    if (keys == 0) return 0.0;
+    if (units == 0) return 0.0;
     if (sms <= 0) return HUGE_VAL;
+    const double ctas = (double)sms * cps;
     const double chunk = std::max(512.0, (double)keys / (2.0 * sms));
     const double items = std::max((double)units, (double)keys / chunk);
     const double bytes = keys * key_bytes;
-    const double one = std::min((double)longest, chunk) * key_bytes / (sm_rate / cps) + kItemDec;
-    return std::max({bytes / hbm, (bytes / sm_rate + items * kItemDec / cps) / sms, one});
+    const double each = std::max(least, item + bytes / items / rate);
+    const double one = std::max(least, item + std::min((double)longest, chunk) * key_bytes / rate);
+    return std::max({bytes / hbm, items * each / ctas, std::min(items, std::ceil(items / ctas)) * each * 0.9, one});
+  }
+
+  // the combine kernel: `rows` part rows of all units, `parts` of the unit with most
+  double combine(double rows, int64_t parts) const {
+    return 3.5 + (parts > 8 ? 0.03 : 0.1) * parts + rows * 2.0 * d * sizeof(float) / 5e6;
   }
 };
 
@@ -153,7 +163,6 @@ SplitChoice choose_split(const pkv_problem& p, const std::vector<PrefixRun>& run
     }
     if (shared[b] > 0) own_rows += (double)lq * p.num_heads_q;
   }
-  const double row_bytes = 2.0 * D * sizeof(float);  // written and read
   SplitChoice best{num_sms, 1 << 30, HUGE_VAL};
   for (int64_t k = 2;; k += std::max<int64_t>(1, k / 4)) {
     const int64_t ch = k * kKvTile;
@@ -177,13 +186,11 @@ SplitChoice choose_split(const pkv_problem& p, const std::vector<PrefixRun>& run
     auto consider = [&](int sms) {
       const double tc = items == 0 ? 0.0
                                    : std::max({most, sum / sms, (double)((items + sms - 1) / sms) * sum / items});
-      // (with no prefix shared: one launch, in which both kinds share every SM)
-      const double t = runs.empty() ? tc + tm.decode(dec.keys, dec.units, dec.longest, num_sms)
-                       : std::max(tc, tm.decode(dec.keys, dec.units, dec.longest, items ? num_sms - sms : num_sms)) +
-                             tm.kParts + rows * row_bytes / tm.kPartRate;
+      const double t = std::max(tc, tm.decode(dec.keys, dec.units, dec.longest, items ? num_sms - sms : num_sms)) +
+                       tm.combine(rows, (longest + ch - 1) / ch + 1);
       if (t < best.time) best = {sms, ch, t};
     };
-    if (dec.keys == 0 || items == 0 || runs.empty() || num_sms < 2) {
+    if (dec.units == 0 || items == 0 || num_sms < 2) {
       consider(num_sms);
     } else {
       for (int sms = std::max(1, num_sms / 38); sms < num_sms; sms += std::max(1, num_sms / 38)) consider(sms);
@@ -192,6 +199,51 @@ SplitChoice choose_split(const pkv_problem& p, const std::vector<PrefixRun>& run
     if (ch >= longest) break;
   }
   return best;
+}
+
+// The time of the batch planned without sharing, by the same model: one launch
+// in which both kinds of tiles share every SM, units cut as make_plan cuts them.
+double plain_time(const pkv_problem& p, const int32_t* q_lens, const int32_t* cache_lens, const int32_t* new_lens,
+                  int num_sms, int n_sub, int tq, int dec_rows) {
+  const int G = p.num_heads_q / p.num_heads_kv;
+  const TimeModel tm(p.head_dim, p.cache_dtype == PKV_FP8_E4M3);
+  DecodeWork dec;
+  double split_keys = 0;
+  bool any_tc = false;
+  for (int b = 0; b < p.batch; ++b) {
+    if (q_lens[b] == 0) continue;
+    const int64_t keys = (int64_t)cache_lens[b] + (new_lens ? new_lens[b] : 0);
+    const bool d = (int64_t)q_lens[b] * G <= dec_rows;
+    if (d) dec.add(keys, p.num_heads_kv);
+    any_tc |= !d;
+    if (d || q_lens[b] <= tq) split_keys += (double)keys * p.num_heads_kv * (d ? 1 : n_sub);
+  }
+  const double chunk = std::max(512.0, split_keys / ((any_tc ? 4.0 : 2.0) * num_sms));
+  double sum = 0, most = 0, part_rows = 0, most_parts = 1;
+  int64_t items = 0;
+  for (int b = 0; b < p.batch; ++b) {
+    const int lq = q_lens[b];
+    if (lq == 0) continue;
+    const int64_t keys = (int64_t)cache_lens[b] + (new_lens ? new_lens[b] : 0);
+    const double parts = std::max(1.0, std::ceil(keys / chunk));
+    const bool d = (int64_t)lq * G <= dec_rows;
+    if (!d) {
+      const bool whole = lq > tq;
+      const int64_t n = (int64_t)p.num_heads_kv * n_sub * (whole ? (lq + tq - 1) / tq : (int64_t)parts);
+      const double t = tm.kItemTc + (whole ? keys : std::min((double)keys, chunk)) / 128.0 * tm.tile1;
+      items += n;
+      sum += n * t;
+      most = std::max(most, t);
+    }
+    if ((d || lq <= tq) && parts > 1) {
+      part_rows += parts * lq * p.num_heads_q;
+      most_parts = std::max(most_parts, parts);
+    }
+  }
+  const double tc =
+      items ? std::max({most, sum / num_sms, (double)((items + num_sms - 1) / num_sms) * sum / items}) : 0.0;
+  return tc + tm.decode(dec.keys, dec.units, dec.longest, num_sms) +
+         (most_parts > 1 ? tm.combine(part_rows, (int64_t)most_parts) : 0.0);
 }
 
 }  // namespace
@@ -338,12 +390,11 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   // Sharing pays once the keys it saves outweigh the parts' combine kernel (four
   // sequences on 512 keys: 11.5 us a call shared, 10.4 not; 64 on 2048: 42 and 98).
   if (!runs.empty() && !groups->always) {
-    const std::vector<int32_t> none(B, 0);
     const double with = choose_split(p, runs, h_q_lens, h_cache_lens, h_new_lens, shared.data(), num_sms, n_sub,
                                      tq_prefill, dec_rows).time;
     const double without =
-        choose_split(p, {}, h_q_lens, h_cache_lens, h_new_lens, none.data(), num_sms, n_sub, tq_prefill, dec_rows).time;
-    if (with >= without) {
+        plain_time(p, h_q_lens, h_cache_lens, h_new_lens, num_sms, n_sub, tq_prefill, dec_rows);
+    if (with >= 0.9 * without) {
       runs.clear();
       shared.assign(B, 0);
     }
@@ -701,8 +752,11 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   bool tc_prefix_only = true;
   for (const Tile& t : tiles) tc_prefix_only &= t.item.kind == kDecode || t.prefix;
   plan->dec_first = apart && cps == 1 && tc_prefix_only;
-  plan->max_combine_rows = 0;
-  for (const CombineItem& c : combines) plan->max_combine_rows = std::max(plan->max_combine_rows, c.n_q * c.nh);
+  plan->max_combine_rows = plan->max_combine_parts = 0;
+  for (const CombineItem& c : combines) {
+    plan->max_combine_rows = std::max(plan->max_combine_rows, c.n_q * c.nh);
+    plan->max_combine_parts = std::max(plan->max_combine_parts, c.nsplit + c.p_nsplit);
+  }
   plan->num_slots = (int32_t)num_slots;
   plan->total_q = (int32_t)total_q;
   plan->total_new = (int32_t)total_new;
@@ -718,6 +772,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   plan->num_combine = (int32_t)combines.size();
   plan->dynamic = dynamic ? 1 : 0;
   plan->shared = runs.empty() ? 0 : 1;
+  plan->row_combine = groups != nullptr;
 
   WorkItem* items = (WorkItem*)(plan->image + L.items);
   int32_t* cta_begin = (int32_t*)(plan->image + L.cta_begin);

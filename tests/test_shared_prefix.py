@@ -331,6 +331,8 @@ CASES = dict(
     page256=dict(starts=[0, 20], prefix=[800], own=rnd.integers(1, 900, 20), q=[1] * 20, page=256),
     ragged=dict(starts=[0, 20], prefix=[480], own=rnd.integers(1, 90, 20), q=[1] * 20, ragged=True),
     many_chunks=dict(starts=[0, 20], prefix=[20000], own=rnd.integers(1, 5000, 20), q=[1] * 20, hq=4, hkv=1),
+    many_chunks_d64=dict(starts=[0, 20], prefix=[20000], own=rnd.integers(1, 50, 20), q=[1] * 20, hq=4, hkv=1, d=64),
+    many_chunks_d256=dict(starts=[0, 20], prefix=[20000], own=rnd.integers(1, 50, 20), q=[1] * 20, hq=4, hkv=1, d=256),
     full=dict(starts=[0, 64], prefix=[6000], own=rnd.integers(1, 1500, 64), q=[1] * 64, hq=32, hkv=8),
     one_sm=dict(starts=[0, 20], prefix=[900], own=rnd.integers(1, 400, 20), q=[1] * 20, num_sms=1),
     few_sms=dict(starts=[0, 20], prefix=[1900], own=rnd.integers(1, 400, 20), q=[1] * 20, num_sms=7),
@@ -461,6 +463,26 @@ def test_calls_between_kernels_that_write_and_read(pkv, gpu, name, fp8):
     torch.cuda.synchronize()
     assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
     assert pkv.get_status(c.ws) == 0
+
+
+@pytest.mark.gpu
+def test_placed_rows_where_nothing_is_shared(pkv, gpu):
+    """A plan that ends up sharing nothing takes query rows placed by the caller, split units among them."""
+    torch = gpu
+    c = Shared(pkv, torch, 19, starts=[0, 3], prefix=[600], own=[5, 9000, 7700], q=[1] * 3, hq=200, hkv=1, shares=False)
+    assert c.run() == 0 and c.plan.stats()["num_split_units"] > 0
+    want, want_lse = c.out.clone(), c.lse.clone()
+    at = [7, 2, 4]                                # rows of the three sequences among nine
+    q = torch.zeros(9, *c.q.shape[1:], dtype=torch.bfloat16, device="cuda")
+    q[at] = c.q
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((c.hq, 9), 7.0, dtype=torch.float32, device="cuda")
+    cu = H.i32(at + [9])
+    pkv.attn_varlen_kvcache_fwd(c.problem, c.args(q=q, out=out, lse=lse, cu_seqlens_q=cu, q_rows=9), c.plan, c.ws)
+    assert pkv.get_status(c.ws) == 0
+    assert torch.equal(out[at], want) and torch.equal(lse[:, at], want_lse)
+    out[at], lse[:, at] = 7.0, 7.0
+    assert torch.all(out == 7.0) and torch.all(lse == 7.0)
 
 
 @pytest.mark.gpu
