@@ -209,9 +209,13 @@ def make_rope_spec(*, cos_sin=None, interleaved=False, eps=1e-6, q_weight=None, 
     rot_dim/2 cosines and then sines of each position (None: no rotation);
     q_weight / k_weight: (head_dim,) bf16 RMS norm weights (None: no norm)."""
     r = RopeSpec(interleaved=int(bool(interleaved)), eps=eps, q_weight=_ptr(q_weight), k_weight=_ptr(k_weight))
+    r.weight_dim = None  # head_dim that the weights are made for
     for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _need(w, what, ("bfloat16",), 1)
+            if r.weight_dim not in (None, w.shape[0]):
+                raise ValueError(f"q_weight and k_weight differ in length ({r.weight_dim}, {w.shape[0]})")
+            r.weight_dim = w.shape[0]
     if cos_sin is not None:
         _need(cos_sin, "cos_sin", ("float32",), 2)
         if cos_sin.shape[0] > 1 and cos_sin.stride(0) != cos_sin.shape[1]:
@@ -258,10 +262,25 @@ def make_rope_append_args(*, spec: RopeSpec, q_out=None) -> RopeAppendArgs:
     """The transform of ``rope_kv_append`` and where its queries go (None: the
     queries are left alone)."""
     r = RopeAppendArgs(spec=spec)
+    r.weight_dim, r.q_shape = getattr(spec, "weight_dim", None), None
     if q_out is not None:
         _need(q_out, "q_out", ("bfloat16",), 3)
+        r.q_shape = tuple(q_out.shape)
         r.q_out, r.qo_stride_tok, r.qo_stride_head = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
     return r
+
+
+def _check_weights(weight_dim, head_dim: int) -> None:
+    if weight_dim is not None and weight_dim != head_dim:
+        raise ValueError(f"norm weights of {weight_dim} values for head_dim {head_dim}")
+
+
+def _check_rope(problem: Problem, rope: RopeAppendArgs, total_q: int) -> None:
+    """The transform's tensors against the problem: what the pointers alone do not tell the library."""
+    _check_weights(getattr(rope, "weight_dim", None), problem.head_dim)
+    shape = getattr(rope, "q_shape", None)
+    if shape is not None and (shape[0] < total_q or shape[1:] != (problem.num_heads_q, problem.head_dim)):
+        raise ValueError(f"q_out {shape}: ({total_q}, {problem.num_heads_q}, {problem.head_dim}) expected")
 
 
 class Plan:
@@ -292,6 +311,7 @@ class Plan:
             _check(fn(*lens, int(num_sms), ctypes.byref(h), ctypes.byref(ws)))
         self.handle = h
         self.workspace_bytes = int(ws.value)
+        self.total_q = int(self._q[:problem.batch].sum())
 
     def stats(self) -> dict:
         s = PlanStats()
@@ -379,6 +399,7 @@ def kv_append(problem: Problem, args: FwdArgs, total_new: int, device_status=Non
 
 def qk_norm_rope(args: QkArgs, spec: RopeSpec, device_status=None, stream=None) -> None:
     """Norm of every head of q and k and the rotation by each token's position, in one pass."""
+    _check_weights(getattr(spec, "weight_dim", None), args.head_dim)
     _check(lib().pkv_qk_norm_rope(ctypes.byref(args), ctypes.byref(spec), _ptr(device_status),
                                   _stream_handle(stream)))
 
@@ -386,6 +407,7 @@ def qk_norm_rope(args: QkArgs, spec: RopeSpec, device_status=None, stream=None) 
 def rope_kv_append(problem: Problem, args: FwdArgs, rope: RopeAppendArgs, total_q: int, total_new: int,
                    device_status=None, stream=None) -> None:
     """``kv_append`` with the norm and rotation on the way into the cache, and of the queries into rope's q_out."""
+    _check_rope(problem, rope, total_q)
     _check(lib().pkv_rope_kv_append(ctypes.byref(problem), ctypes.byref(args), ctypes.byref(rope), int(total_q),
                                     int(total_new), _ptr(device_status), _stream_handle(stream)))
 
@@ -393,6 +415,7 @@ def rope_kv_append(problem: Problem, args: FwdArgs, rope: RopeAppendArgs, total_
 def rope_attn_varlen_kvcache_fwd(problem: Problem, args: FwdArgs, rope: RopeAppendArgs, plan_: Plan, workspace,
                                  stream=None) -> None:
     """The attention call with ``rope_kv_append`` in place of its append."""
+    _check_rope(problem, rope, plan_.total_q)
     _check(lib().pkv_rope_attn_varlen_kvcache_fwd(ctypes.byref(problem), ctypes.byref(args), ctypes.byref(rope),
                                                   plan_.handle, workspace.data_ptr(),
                                                   workspace.numel() * workspace.element_size(),

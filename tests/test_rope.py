@@ -121,6 +121,25 @@ def test_binding_refuses_wrong_tensors(pkv):
         pkv.make_rope_spec(q_weight=_Fake((64,), "float32"))
 
 
+def test_binding_checks_the_transform_against_the_problem(pkv):
+    """Weights of another head_dim, an output too small for the queries: refused before anything is launched."""
+    with pytest.raises(ValueError):
+        pkv.make_rope_spec(q_weight=_Fake((64,)), k_weight=_Fake((128,)))
+    short = pkv.make_rope_spec(q_weight=_Fake((32,)))
+    with pytest.raises(ValueError):
+        pkv.qk_norm_rope(pkv.make_qk_args(q=_Fake((5, 4, 64))), short, stream=0)
+    prob, args, _, _ = _append_call(pkv)
+    pl = pkv.plan(prob, [3, 1], [37, 5], [3, 1], num_sms=4)
+    table = pkv.make_rope_spec(cos_sin=_Fake((64, 64), "float32"))
+    for spec, q_out in ((short, _Fake((4, 4, 64))), (table, _Fake((3, 4, 64))), (table, _Fake((4, 2, 64))),
+                        (table, _Fake((4, 4, 128)))):
+        rope = pkv.make_rope_append_args(spec=spec, q_out=q_out)
+        with pytest.raises(ValueError):
+            pkv.rope_kv_append(prob, args, rope, 4, 4, stream=0)
+        with pytest.raises(ValueError):
+            pkv.rope_attn_varlen_kvcache_fwd(prob, args, rope, pl, None, stream=0)
+
+
 def _append_call(pkv, **over):
     """Good arguments of the rotating append over fake tensors, with changes."""
     q, k = _Fake((4, 4, 64)), _Fake((4, 2, 64), ptr=1 << 22)
