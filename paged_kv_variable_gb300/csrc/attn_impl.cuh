@@ -1279,6 +1279,8 @@ __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* sm
       // The softmax runs up to kSBufs tiles ahead of P V; with fewer V stages
       // (D = 256) the stage may still wait for its previous tile, whose
       // unfinished phase would pass for this one's: that tile's P V first.
+      // (With decode tiles between the two, the stage last held one of those,
+      // which these warps have used, or a tile whose P V they waited for.)
       if constexpr (!L::kQQ && L::kStagesV < L::kSBufs) {
         if (T >= (uint32_t)L::kStagesV &&
             !warp_wait(&B.o_done[(T - L::kStagesV) % L::kSBufs], ((T - L::kStagesV) / L::kSBufs) & 1, abort_flag))
@@ -1392,7 +1394,8 @@ __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* sm
 // last V stage serving as the merge scratch.
 template <int D, bool FP8, bool PF, bool QF8, int NQ>
 __device__ bool run_decode(const AttnParams& p, const WorkItem& w, uint8_t* smem, const Bars& B,
-                           volatile int* abort_flag, Ring& rk, Ring& rv, float sl2, float vscale, uint32_t& dtc) {
+                           volatile int* abort_flag, Ring& rk, Ring& rv, float sl2, float vscale, uint32_t& dtc,
+                           bool failed) {
   using L = Layout<D, FP8, PF>;
   constexpr bool kArea = L::kStageRegs;          // the merge area exists (else: the borrowed V stage)
   constexpr bool kRegs = L::kStageRegs && NQ == 1;  // tiles staged in registers (no room at NQ = 2)
@@ -1488,10 +1491,9 @@ __device__ bool run_decode(const AttnParams& p, const WorkItem& w, uint8_t* smem
   int merge_stage = -1;
   // A failed (timed-out or aborted) wait ends this warp's tiles, but the warp
   // still passes every barrier of the merge below, so that no other consumer
-  // warp can be left waiting there.
-  bool failed = false;
-
-  for (int t0 = w.kv_begin; t0 < w.kv_end; t0 += kTile) {
+  // warp can be left waiting there (nor by a warp that failed in an earlier
+  // item, which comes here with `failed` set and runs no tile).
+  for (int t0 = failed ? w.kv_end : w.kv_begin; t0 < w.kv_end; t0 += kTile) {
     const bool mine = L::kDecGroups == 1 || (int)(dtc % L::kDecGroups) == gi;
     ++dtc;
     if (!mine) {  // the other group's tile: every warp advances the rings over all tiles
@@ -1926,6 +1928,9 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
   uint32_t pt = 0;
   uint32_t dtc = 0;  // decode tiles seen (consumer groups take alternate ones)
   PendingEpi pend;
+  // this warp failed in a prefill item (instances with both kinds of tiles): it
+  // only passes the barriers of the decode items that are left
+  bool failed = false;
   for (int it = it0; it < it1; ++it) {
     const WorkItem w = load_item(p, it);
     if (it + 1 < it1) {
@@ -1940,10 +1945,21 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
         // (at D = 256 the plan gives decode tiles at most 8 rows)
         // (a kernel built without decode tiles never receives them)
         if constexpr (DEC) {
+          // The softmax ends a prefill item before its last P V, whose V tiles
+          // may still be on their way.  A decode tile's V stage last held one
+          // of them, and while that use is unfinished its barrier reads as if
+          // this tile's had completed: the last P V (and so every V tile of
+          // the item) first.
+          if constexpr (PF) {
+            if (!failed && pend.has)
+              failed = !warp_wait(&B.o_done[pend.T % L::kSBufs], (pend.T / L::kSBufs) & 1, abort_flag);
+          }
           if (D > 128 || w.n_q * p.G <= 8)
-            ok = run_decode<D, FP8, PF, QF8, 1>(p, w, smem, B, abort_flag, rk, rv, QF8 ? sl2q : sl2, vscale, dtc);
+            ok = run_decode<D, FP8, PF, QF8, 1>(p, w, smem, B, abort_flag, rk, rv, QF8 ? sl2q : sl2, vscale, dtc,
+                                                failed);
           else if constexpr (D <= 128)
-            ok = run_decode<D, FP8, PF, QF8, 2>(p, w, smem, B, abort_flag, rk, rv, QF8 ? sl2q : sl2, vscale, dtc);
+            ok = run_decode<D, FP8, PF, QF8, 2>(p, w, smem, B, abort_flag, rk, rv, QF8 ? sl2q : sl2, vscale, dtc,
+                                                failed);
         } else {
           ok = false;
         }
@@ -1957,19 +1973,21 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
       const int qt = L::kQQ ? ((threadIdx.x >> 5) - L::kCons0) >> 2 : 0;
       const WorkItem wq = L::kQQ ? q_tile(w, qt, p.causal) : w;
       const bool zero_owner = !L::kQQ || qt == 1 || num_tiles<L::kTile>(q_tile(w, 1, p.causal)) == 0;
-      ok = softmax_item<D, FP8, PF>(p, wq, smem, B, abort_flag, tmem, rk, rv, pt, QF8 ? sl2q : sl2, vscale, pend, qt,
-                                    num_tiles<L::kTile>(w), zero_owner);
+      if (!failed)
+        ok = softmax_item<D, FP8, PF>(p, wq, smem, B, abort_flag, tmem, rk, rv, pt, QF8 ? sl2q : sl2, vscale, pend, qt,
+                                      num_tiles<L::kTile>(w), zero_owner);
     } else {
       ok = false;  // a decode-only launch never receives prefill tiles
     }
     if (!ok) {
       record_status(p.status, PKV_ERR_DEVICE_TIMEOUT, blockIdx.x, it);
       *abort_flag = 1;
-      return false;
+      if constexpr (!(PF && DEC)) return false;
+      failed = true;
     }
   }
   if constexpr (PF) {
-    if (pend.has) {
+    if (pend.has && !failed) {
       // the last prefill item's epilogue
       const int qw = (threadIdx.x >> 5) & 3;
       const int qt = L::kQQ ? ((threadIdx.x >> 5) - L::kCons0) >> 2 : 0;
