@@ -575,7 +575,16 @@ __device__ void producer(const AttnParams& p, const CUtensorMap* tm_kv, const CU
 // the first converted-K buffer) and S = Q K^T runs as kind::f8f6f4 MMAs on the
 // raw e4m3 K stage, which this thread releases when the MMAs have completed;
 // the converters then turn only V into f16.
-template <int D, bool FP8, bool PF, bool QF8>
+//
+// DEC: decode tiles may lie between prefill items.  The roles that take no part
+// in them (S issuer, converters) step over them without seeing their stages
+// fill, and reach the next prefill item while the consumers still work on them.
+// A stage whose decode tile has not landed by then would read as full (its
+// barrier is two phases behind, the same parity), so the first use of each
+// stage after decode tiles waits for the stage's release by the use before, as
+// the producer does.  (The stage cannot run ahead of that wait: its next
+// release needs this role.)
+template <int D, bool FP8, bool PF, bool QF8, bool DEC>
 __device__ bool s_issuer(const AttnParams& p, uint8_t* smem, const Bars& B, volatile int* abort_flag, uint32_t tmem,
                          int it0, int it1) {
   using L = Layout<D, FP8, PF>;
@@ -585,11 +594,13 @@ __device__ bool s_issuer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
   const uint32_t q_base = smem_u32(smem + (QF8 ? L::kKcOff : L::kQOff));
   Ring rk;
   uint32_t pt = 0, pi = 0;
+  int unseen = 0;  // K stages whose last use this thread has not seen
   for (int it = it0; it < it1; ++it) {
     const WorkItem w = load_item(p, it);
     const int n = num_tiles<L::kTile>(w);
     if (w.kind != kPrefill) {
       rk.advance<L::kStagesK>(n);
+      unseen = L::kStagesK;
       continue;
     }
     if (n == 0) continue;
@@ -602,6 +613,10 @@ __device__ bool s_issuer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
         if (!mbar_wait(&B.kc_full[T % NB], (T / NB) & 1, abort_flag)) return false;
         k_base = smem_u32(smem + L::kKcOff + (T % NB) * L::kConvTile);
       } else {
+        if (DEC && unseen > 0) {
+          --unseen;
+          if (!mbar_wait(&B.empty_k[rk.stage], rk.phase ^ 1, abort_flag)) return false;
+        }
         if (!mbar_wait(&B.full_k[rk.stage], rk.phase, abort_flag)) return false;
         k_base = smem_u32(smem + L::kKOff + rk.stage * L::kTileBytes);
       }
@@ -710,7 +725,7 @@ __device__ bool pv_issuer(const AttnParams& p, uint8_t* smem, const Bars& B, vol
 // the second tile's, which always reaches the item's last K/V tile) both P
 // are waited for first.  So one query tile's MMAs run while the other's
 // softmax does.
-template <int D, bool FP8, bool PF, bool QF8>
+template <int D, bool FP8, bool PF, bool QF8, bool DEC>
 __device__ bool s_issuer_qq(const AttnParams& p, uint8_t* smem, const Bars& B, volatile int* abort_flag, uint32_t tmem,
                             int it0, int it1) {
   using L = Layout<D, FP8, PF>;
@@ -720,11 +735,13 @@ __device__ bool s_issuer_qq(const AttnParams& p, uint8_t* smem, const Bars& B, v
   constexpr int NB = L::kConvBufsK;
   Ring rk;
   uint32_t pt[2] = {0, 0}, pi[2] = {0, 0}, ck = 0;  // S tiles and items per query tile; K tiles (converted)
+  int unseen = 0;  // K stages whose last use this thread has not seen
   for (int it = it0; it < it1; ++it) {
     const WorkItem w = load_item(p, it);
     const int n = num_tiles<kTile>(w);
     if (w.kind != kPrefill) {
       rk.advance<L::kStagesK>(n);
+      unseen = L::kStagesK;
       continue;
     }
     if (n == 0) continue;
@@ -742,6 +759,10 @@ __device__ bool s_issuer_qq(const AttnParams& p, uint8_t* smem, const Bars& B, v
         if (!mbar_wait(&B.kc_full[ck % NB], (ck / NB) & 1, abort_flag)) return false;
         k_base = smem_u32(smem + L::kKcOff + (ck % NB) * L::kConvTile);
       } else {
+        if (DEC && unseen > 0) {
+          --unseen;
+          if (!mbar_wait(&B.empty_k[rk.stage], rk.phase ^ 1, abort_flag)) return false;
+        }
         if (!mbar_wait(&B.full_k[rk.stage], rk.phase, abort_flag)) return false;
         k_base = smem_u32(smem + L::kKOff + rk.stage * L::kTileBytes);
       }
@@ -905,7 +926,7 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* conv, 
   }
 }
 
-template <int D, bool PF, bool QF8>
+template <int D, bool PF, bool QF8, bool DEC>
 __device__ bool converter(const AttnParams& p, uint8_t* smem, const Bars& B, volatile int* abort_flag, int it0,
                           int it1) {
   using L = Layout<D, true, PF>;
@@ -913,12 +934,15 @@ __device__ bool converter(const AttnParams& p, uint8_t* smem, const Bars& B, vol
   const int ct = threadIdx.x - 32 * L::kConvWarp0;  // 0..127
   Ring rk, rv;
   uint32_t pt = 0, pi[2] = {0, 0};
+  static_assert(L::kStagesK == L::kStagesV, "stages");
+  int unseen = 0;  // K and V stages whose last use these warps have not seen (s_issuer)
   for (int it = it0; it < it1; ++it) {
     const WorkItem w = load_item(p, it);
     const int n = num_tiles<L::kTile>(w);
     if (w.kind != kPrefill) {
       rk.advance<L::kStagesK>(n);
       rv.advance<L::kStagesV>(n);
+      unseen = L::kStagesK;
       continue;
     }
     if (n == 0) continue;
@@ -971,7 +995,10 @@ __device__ bool converter(const AttnParams& p, uint8_t* smem, const Bars& B, vol
     for (int j = 0; j < n; ++j) {
       const uint32_t T = pt + j;
       const int t0 = w.kv_begin + j * L::kTile;
+      const bool first_use = DEC && unseen > 0;
+      if (first_use) --unseen;
       if constexpr (!QF8) {
+        if (first_use && !warp_wait(&B.empty_k[rk.stage], rk.phase ^ 1, abort_flag)) return false;
         if (!warp_wait(&B.full_k[rk.stage], rk.phase, abort_flag)) return false;
         if (T >= NB && !warp_wait(&B.kc_empty[T % NB], ((T / NB) - 1) & 1, abort_flag)) return false;
         convert_tile<D, L::kTile>(smem + L::kKOff + rk.stage * L::kTileBytes, smem + L::kKcOff + (T % NB) * L::kConvTile,
@@ -983,6 +1010,7 @@ __device__ bool converter(const AttnParams& p, uint8_t* smem, const Bars& B, vol
           mbar_arrive(&B.empty_k[rk.stage]);
         }
       }
+      if (first_use && !warp_wait(&B.empty_v[rv.stage], rv.phase ^ 1, abort_flag)) return false;
       if (!warp_wait(&B.full_v[rv.stage], rv.phase, abort_flag)) return false;
       if (T >= NV && !warp_wait(&B.vc_empty[T % NV], ((T / NV) - 1) & 1, abort_flag)) return false;
       // rows past the sequence may hold anything (even NaN): they become zeros
@@ -2117,10 +2145,10 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
         bool ok;
         if constexpr (L::kQQ)
           ok = pv ? pv_issuer_qq<D, FP8, PF>(p, smem, B, abort_flag, tmem, it0, it1)
-                  : s_issuer_qq<D, FP8, PF, QF8>(p, smem, B, abort_flag, tmem, it0, it1);
+                  : s_issuer_qq<D, FP8, PF, QF8, DEC>(p, smem, B, abort_flag, tmem, it0, it1);
         else
           ok = pv ? pv_issuer<D, FP8, PF>(p, smem, B, abort_flag, tmem, it0, it1)
-                  : s_issuer<D, FP8, PF, QF8>(p, smem, B, abort_flag, tmem, it0, it1);
+                  : s_issuer<D, FP8, PF, QF8, DEC>(p, smem, B, abort_flag, tmem, it0, it1);
         if (!ok) {
           record_status(p.status, PKV_ERR_DEVICE_TIMEOUT, blockIdx.x, pv ? -3 : -1);
           *abort_flag = 1;
@@ -2134,7 +2162,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
       if constexpr (L::kConvWarps > 0) {
         if constexpr (L::kRegsConv > L::kLaunchRegs) reg_alloc<L::kRegsConv>();
         else reg_dealloc<L::kRegsConv>();
-        if (!converter<D, PF, QF8>(p, smem, B, abort_flag, it0, it1)) {
+        if (!converter<D, PF, QF8, DEC>(p, smem, B, abort_flag, it0, it1)) {
           if (lane == 0) record_status(p.status, PKV_ERR_DEVICE_TIMEOUT, blockIdx.x, -2);
           *abort_flag = 1;
         }
@@ -2162,7 +2190,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
   }
   if constexpr (L::kConvWarps > 0) {
     if (warp >= L::kConvWarp0 && warp < L::kConvWarp0 + L::kConvWarps) {
-      if (!converter<D, PF, QF8>(p, smem, B, abort_flag, it0, it1)) {
+      if (!converter<D, PF, QF8, DEC>(p, smem, B, abort_flag, it0, it1)) {
         if (lane == 0) record_status(p.status, PKV_ERR_DEVICE_TIMEOUT, blockIdx.x, -2);
         *abort_flag = 1;
       }
@@ -2174,7 +2202,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
       if (lane == 0) {
         const bool pv = warp == L::kPvWarp;
         if (!(pv ? pv_issuer<D, FP8, PF>(p, smem, B, abort_flag, tmem, it0, it1)
-                 : s_issuer<D, FP8, PF, QF8>(p, smem, B, abort_flag, tmem, it0, it1))) {
+                 : s_issuer<D, FP8, PF, QF8, DEC>(p, smem, B, abort_flag, tmem, it0, it1))) {
           record_status(p.status, PKV_ERR_DEVICE_TIMEOUT, blockIdx.x, pv ? -3 : -1);
           *abort_flag = 1;
           // wait (bounded) for this thread's MMAs already issued before the memory is freed

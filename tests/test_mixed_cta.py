@@ -84,3 +84,41 @@ def test_decode_after_prefill(d, dtype, q8, causal, lk, P):
     kinds = run_on_one_cta(case)
     turn = kinds.index(DECODE)
     assert turn > 0 and set(kinds[:turn]) == {PREFILL} and set(kinds[turn:]) == {DECODE}
+
+
+def _decode_keys(d, dtype, cost):
+    """Keys of a decode unit that the plan rates at about `cost` (model units)."""
+    return int((cost - 64) * 512 / (2 * d * (1 if dtype == "fp8" else 2)))
+
+
+@pytest.mark.parametrize("P", [1, 4, 16])
+@pytest.mark.parametrize("extra", [0, 65, 130, 254])
+@pytest.mark.parametrize("d,dtype,q8", FORMS)
+def test_prefill_after_decode(d, dtype, q8, extra, P):
+    """Decode units, then short prompts: the warps that take no part in decode tiles
+    (the S issuer, the converters) reach the prompt's first tiles while the decode
+    tiles that fill the same stages may still be on their way."""
+    n = _decode_keys(d, dtype, 420 + 130 * d // 128) + extra
+    case = mixed_case(d, dtype, P, True, [1, 130, 1, 70, 2, 129], [n, 0, n + 67, 0, n + 128, 0], q8)
+    kinds = run_on_one_cta(case)
+    turn = kinds.index(PREFILL)
+    assert turn > 0 and set(kinds[:turn]) == {DECODE} and set(kinds[turn:]) == {PREFILL}
+
+
+@pytest.mark.parametrize("P", [1, 16])
+@pytest.mark.parametrize("seed", range(3))
+@pytest.mark.parametrize("d,dtype,q8", FORMS)
+def test_kinds_in_turn(d, dtype, q8, seed, P):
+    """Decode units and prompts alternating, some of a single tile."""
+    rng = np.random.default_rng(seed)
+    q_lens, cache_lens = [], []
+    for cost in rng.permutation(np.arange(330, 330 + 8 * 40, 40)):
+        keys = _decode_keys(d, dtype, cost) + int(rng.integers(0, 8))
+        if dtype == "bf16" or keys > 20:
+            q_lens.append(1)
+            cache_lens.append(keys)
+        q_lens.append(int(rng.integers(65, 75)))
+        cache_lens.append(max(0, int((cost - 256) * 128 / d) - 40 + int(rng.integers(0, 5))))
+    case = mixed_case(d, dtype, P, bool(seed % 2), q_lens, cache_lens, q8)
+    kinds = run_on_one_cta(case)
+    assert sum(a != b for a, b in zip(kinds, kinds[1:])) >= 6
