@@ -1519,8 +1519,7 @@ __device__ bool run_decode(const AttnParams& p, const WorkItem& w, uint8_t* smem
   int merge_stage = -1;
   // A failed (timed-out or aborted) wait ends this warp's tiles, but the warp
   // still passes every barrier of the merge below, so that no other consumer
-  // warp can be left waiting there (nor by a warp that failed in an earlier
-  // item, which comes here with `failed` set and runs no tile).
+  // warp can be left waiting there.
   for (int t0 = failed ? w.kv_end : w.kv_begin; t0 < w.kv_end; t0 += kTile) {
     const bool mine = L::kDecGroups == 1 || (int)(dtc % L::kDecGroups) == gi;
     ++dtc;
@@ -1935,6 +1934,24 @@ __device__ bool run_decode(const AttnParams& p, const WorkItem& w, uint8_t* smem
   return !any_bad;
 }
 
+// A consumer warp that has failed and will run no more items (instances with
+// both kinds of tiles, whose warps may fail one by one in a prefill item): the
+// barriers of the decode items that are left, so that no other warp can be left
+// waiting at one.  (Out of line, away from the loop: a flag that the loop carried
+// cost the mixed batch 3%.)
+template <int D, bool FP8, bool PF>
+__device__ __noinline__ void pass_merges(const AttnParams& p, uint8_t* smem, int it0, int it1) {
+  using L = Layout<D, FP8, PF>;
+  static_assert(!L::kStageRegs && L::kDecWarps == 4, "the tree merge of four warps: six barriers");
+  int* bad = reinterpret_cast<int*>(smem + L::kMlOff) + L::kDecWarps * kDecodeRows * 2;
+  for (int it = it0; it < it1; ++it) {
+    const WorkItem w = load_item(p, it);
+    if (w.kind != kDecode || num_tiles<L::kTile>(w) == 0) continue;
+    if ((threadIdx.x & 31) == 0) bad[(threadIdx.x >> 5) - L::kCons0] = 1;
+    for (int k = 0; k < 6; ++k) named_bar_sync(1, 32 * L::kDecWarps);
+  }
+}
+
 template <int D, bool FP8, bool PF, bool QF8, bool DEC>
 __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, volatile int* abort_flag, uint32_t tmem,
                          int it0, int it1) {
@@ -1956,9 +1973,6 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
   uint32_t pt = 0;
   uint32_t dtc = 0;  // decode tiles seen (consumer groups take alternate ones)
   PendingEpi pend;
-  // this warp failed in a prefill item (instances with both kinds of tiles): it
-  // only passes the barriers of the decode items that are left
-  bool failed = false;
   for (int it = it0; it < it1; ++it) {
     const WorkItem w = load_item(p, it);
     if (it + 1 < it1) {
@@ -1978,8 +1992,9 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
           // of them, and while that use is unfinished its barrier reads as if
           // this tile's had completed: the last P V (and so every V tile of
           // the item) first.
+          bool failed = false;
           if constexpr (PF) {
-            if (!failed && pend.has)
+            if (pend.has)
               failed = !warp_wait(&B.o_done[pend.T % L::kSBufs], (pend.T / L::kSBufs) & 1, abort_flag);
           }
           if (D > 128 || w.n_q * p.G <= 8)
@@ -2001,21 +2016,23 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
       const int qt = L::kQQ ? ((threadIdx.x >> 5) - L::kCons0) >> 2 : 0;
       const WorkItem wq = L::kQQ ? q_tile(w, qt, p.causal) : w;
       const bool zero_owner = !L::kQQ || qt == 1 || num_tiles<L::kTile>(q_tile(w, 1, p.causal)) == 0;
-      if (!failed)
-        ok = softmax_item<D, FP8, PF>(p, wq, smem, B, abort_flag, tmem, rk, rv, pt, QF8 ? sl2q : sl2, vscale, pend, qt,
-                                      num_tiles<L::kTile>(w), zero_owner);
+      ok = softmax_item<D, FP8, PF>(p, wq, smem, B, abort_flag, tmem, rk, rv, pt, QF8 ? sl2q : sl2, vscale, pend, qt,
+                                    num_tiles<L::kTile>(w), zero_owner);
     } else {
       ok = false;  // a decode-only launch never receives prefill tiles
     }
     if (!ok) {
       record_status(p.status, PKV_ERR_DEVICE_TIMEOUT, blockIdx.x, it);
       *abort_flag = 1;
-      if constexpr (!(PF && DEC)) return false;
-      failed = true;
+      // the decode items that are left have barriers that the other warps may come to
+      if constexpr (PF && DEC) {
+        if (mma_consumer) pass_merges<D, FP8, PF>(p, smem, it + 1, it1);
+      }
+      return false;
     }
   }
   if constexpr (PF) {
-    if (pend.has && !failed) {
+    if (pend.has) {
       // the last prefill item's epilogue
       const int qw = (threadIdx.x >> 5) & 3;
       const int qt = L::kQQ ? ((threadIdx.x >> 5) - L::kCons0) >> 2 : 0;
