@@ -39,9 +39,10 @@
  *    key gets out = 0 and lse = -inf.
  *  - Head mapping: query head h reads kv head h / (Hq / Hkv).
  *  - stream arguments are cudaStream_t passed as void* (NULL = legacy stream).
- *  - A call's first kernel may be launched while the stream's previous kernel
- *    drains (programmatic stream serialization); it waits for that kernel before
- *    it reads or writes anything.
+ *  - A call follows everything that was put on its stream before it: its first
+ *    kernel is an ordinary launch.  Its other kernels may start while the one
+ *    before them in the call drains (programmatic stream serialization), and
+ *    wait for it before they read what it writes.
  *  - Errors: every entry point returns a pkv_status.  Problems detectable on
  *    the host are reported before anything is launched.  Problems found on the
  *    device (a block_table entry out of range, an append past the capacity, a

@@ -516,13 +516,14 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
   const bool overlap = plan->num_prefill_items == 0;
   const bool fp8 = pr.cache_dtype == PKV_FP8_E4M3;
   const bool append_overlaps = plan->total_new > 0 && !rope && !g_ev_start;
-  // Without an append, or after the rotating one (whose queries it reads from its
-  // start), the attention starts while the stream's previous kernel drains and
-  // waits for it before it reads anything (decode-only plans and those with
-  // shared prefixes, where the instance can).
+  // After the rotating append, whose queries it reads from its start, the
+  // attention starts while that kernel drains and waits for it before it reads
+  // anything (decode-only plans and those with shared prefixes, where the
+  // instance can).  Without an append it is the call's first kernel, an ordinary
+  // launch: a kernel before the call that was itself started early, and does not
+  // wait, would hide what came before it.
   const bool first_pf = plan->num_ctas_tc > 0 ? !plan->dec_first : plan->num_prefill_items > 0;
-  const bool first = (plan->total_new == 0 || rope) && !g_ev_start && (overlap || plan->shared) &&
-                     starts_early(pr.head_dim, fp8, first_pf);
+  const bool first = rope && !g_ev_start && (overlap || plan->shared) && starts_early(pr.head_dim, fp8, first_pf);
   p.dep_first = first;
   if (plan->num_ctas_tc > 0) {
     // A plan with shared prefixes and both kinds of tiles: the tensor-core tiles

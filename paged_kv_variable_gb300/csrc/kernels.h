@@ -103,7 +103,7 @@ struct AttnParams {
   const int32_t* plan_lc;
   int32_t batch;
   int32_t dynamic;     // plan_lc holds bounds; the cache lengths come from cache_seqlens
-  int32_t dep_first;   // launched while the stream's previous kernel drains: wait for it before anything is read
+  int32_t dep_first;   // launched while the call's rotating append drains: wait for it before anything is read
   int32_t dep_late;    // nothing this launch reads comes from the kernel it overlaps
 };
 

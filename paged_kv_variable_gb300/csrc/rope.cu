@@ -114,10 +114,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const _
   constexpr int kLanes = D / 8;          // lanes of a head
   constexpr int kHeads = 32 / kLanes;    // heads side by side in a warp
   constexpr int kRun = kHeads * HC;      // heads of a warp
-  // launched while the stream's previous kernel drains (2000 ragged tokens 12.4 ->
-  // 10.6 us, 4093 tokens 16.6 -> 14.9): wait for it before anything is read
-  grid_dep_wait();
-  grid_dep_launch();
+  // (an ordinary launch, behind everything on the stream; the attention of the
+  // same call may start now, and waits for this kernel before it reads anything)
+  if constexpr (APPEND) grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const int l = lane % kLanes, sub = lane / kLanes;
   const int uq = (p.hq + kRun - 1) / kRun, uk = (p.a.hkv + kRun - 1) / kRun;
@@ -255,15 +254,10 @@ cudaError_t launch_run(const RopeParams& p, cudaStream_t stream) {
   const int64_t blocks = (tokens + kRopeWarps - 1) / kRopeWarps * (uq + (APPEND ? 2 : 1) * uk);
   if (blocks == 0) return cudaSuccess;
   if (blocks > INT32_MAX || tokens > INT32_MAX - kRopeWarps) return cudaErrorInvalidValue;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3((unsigned)kRopeThreads);
   cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, rope_kernel<D, APPEND, FP8, PAIRS, HC>, p);
 }
 
