@@ -518,12 +518,12 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
   const bool append_overlaps = plan->total_new > 0 && !rope && !g_ev_start;
   // After the rotating append, whose queries it reads from its start, the
   // attention starts while that kernel drains and waits for it before it reads
-  // anything (decode-only plans and those with shared prefixes, where the
-  // instance can).  Without an append it is the call's first kernel, an ordinary
-  // launch: a kernel before the call that was itself started early, and does not
-  // wait, would hide what came before it.
+  // anything (where the first launch is of decode tiles alone).  Without an
+  // append it is the call's first kernel, an ordinary launch: a kernel before the
+  // call that was itself started early, and does not wait, would hide what came
+  // before it.
   const bool first_pf = plan->num_ctas_tc > 0 ? !plan->dec_first : plan->num_prefill_items > 0;
-  const bool first = rope && !g_ev_start && (overlap || plan->shared) && starts_early(pr.head_dim, fp8, first_pf);
+  const bool first = rope && !g_ev_start && !first_pf;
   p.dep_first = first;
   if (plan->num_ctas_tc > 0) {
     // A plan with shared prefixes and both kinds of tiles: the tensor-core tiles
@@ -542,8 +542,7 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
         e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, true, s);
     } else {
       // the append is complete before the first launch starts
-      e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, first, s);
-      pd.dep_first = 0;
+      e = launch_attention(p, tk, tv, tq, plan->num_ctas_tc, pr.head_dim, fp8, true, false, false, s);
       pd.dep_late = 1;
       if (e == cudaSuccess)
         e = launch_attention(pd, tk, tv, tq, dec_ctas, pr.head_dim, fp8, false, true, true, s);

@@ -51,13 +51,6 @@ PKV_HOST_DEVICE inline int tc_group_heads(int G) { return G < kPrefillRowsTc ? G
 // pairs tiles only in plans without decode tiles.
 PKV_HOST_DEVICE constexpr int prefill_q_tiles(int head_dim, bool fp8) { return fp8 && head_dim <= 128 ? 2 : 1; }
 
-// Kernel instances that can be launched while the call's rotating append
-// drains: not the bf16 ones with prefill tiles at head dims 128 and 256, whose
-// softmax lost 2% to the branch (131 -> 135 us on the cached-prefix batch).
-PKV_HOST_DEVICE constexpr bool starts_early(int head_dim, bool fp8, bool prefill) {
-  return !prefill || fp8 || head_dim == 64;
-}
-
 // lk of a tile over a shared prefix (whose rows may belong to several
 // sequences; b is the first of them): past every key, whatever the current
 // lengths, so each of its queries sees all its keys.  (A prefix is whole pages:
