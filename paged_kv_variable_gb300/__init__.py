@@ -8,6 +8,7 @@ the library has not been built, importing works but every call raises
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -35,6 +36,13 @@ class PkvError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
         self.status = status
+
+
+class PkvInputError(PkvError, ValueError):
+    """Refused by the binding: tensors that do not serve the call (the library sees their addresses alone)."""
+
+    def __init__(self, msg: str):
+        super().__init__(1, msg)
 
 
 class Problem(ctypes.Structure):
@@ -172,6 +180,14 @@ def make_args(*, q, out, cu_seqlens_q, max_seqlen_q, k_cache, v_cache, cache_seq
               page_indptr=None, q_scale=None, q_rows=0) -> FwdArgs:
     """Pointers and element strides of torch tensors laid out as in pkv.h."""
     a = FwdArgs()
+    _same_layout(k_new, v_new, "k_new", "v_new")
+    _same_layout(k_cache, v_cache, "k_cache", "v_cache")
+    # what the calls compare with the problem and the counts of tokens, of each
+    # tensor whose address the struct still holds by then
+    a.given = {what: (t.data_ptr(), tuple(t.shape), str(getattr(t, "dtype", "bfloat16")).removeprefix("torch."))
+               for what, t in (("q", q), ("out", out), ("lse", lse), ("k_new", k_new), ("v_new", v_new))
+               if t is not None}
+    a.checked = None  # the last call that they were found to serve
     if q is not None:
         a.q, a.q_stride_tok, a.q_stride_head = q.data_ptr(), q.stride(0), q.stride(1)
     if out is not None:
@@ -194,6 +210,45 @@ def make_args(*, q, out, cu_seqlens_q, max_seqlen_q, k_cache, v_cache, cache_seq
     a.q_scale = _ptr(q_scale)
     a.q_rows = int(q_rows)
     return a
+
+
+def _same_layout(x, y, what_x: str, what_y: str) -> None:
+    """Raises ValueError unless y has the shape of x and its strides, which serve both."""
+    if x is None or y is None:
+        return
+    if tuple(x.shape) != tuple(y.shape) or any(n > 1 and x.stride(i) != y.stride(i) for i, n in enumerate(x.shape)):
+        raise PkvInputError(f"{what_y} must have the shape and strides of {what_x}")
+
+
+def _check_rows(problem: Problem, args: FwdArgs, total_q: int, total_new: int, bf16: bool = False) -> None:
+    """The tensors of make_args against the rows that the call reads and writes:
+    q and out (rows, Hq, D), k_new and v_new (rows, Hkv, D), lse (Hq, rows), with
+    at least so many rows and heads.  Structs that were not made by make_args, and
+    addresses put in since, are taken as they are."""
+    given = getattr(args, "given", None)
+    call = (total_q, total_new, problem.num_heads_q, problem.num_heads_kv, problem.head_dim, bf16)
+    if given is None or call == args.checked:
+        return
+    d = problem.head_dim
+    for what, rows, heads in (("q", total_q, problem.num_heads_q), ("out", total_q, problem.num_heads_q),
+                              ("k_new", total_new, problem.num_heads_kv), ("v_new", total_new, problem.num_heads_kv)):
+        if rows > 0 and what in given:
+            ptr, shape, dtype = given[what]
+            if ((len(shape) != 3 or shape[0] < rows or shape[1] < heads or shape[2] != d)
+                    and getattr(args, what) == ptr):
+                raise PkvInputError(f"{what} {shape}: ({rows}, {heads}, {d}) expected")
+            if bf16 and dtype != "bfloat16" and getattr(args, what) == ptr:
+                raise PkvInputError(f"{what}: bfloat16 expected, got {dtype}")
+    if total_q > 0 and "lse" in given:
+        ptr, shape, _ = given["lse"]
+        if math.prod(shape) < problem.num_heads_q * total_q and args.lse == ptr:
+            raise PkvInputError(f"lse {shape}: ({problem.num_heads_q}, {total_q}) expected")
+    args.checked = call
+
+
+def _check_status_words(device_status) -> None:
+    if device_status is not None and device_status.numel() * device_status.element_size() < 12:
+        raise PkvInputError("device_status: three int32 expected")
 
 
 def _need(t, what: str, dtypes: tuple, ndim: int) -> None:
@@ -290,7 +345,7 @@ class Plan:
                  shared=None):
         import numpy as np
         for what, lens in (("q_lens", q_lens), ("cache_lens", cache_lens), ("new_lens", new_lens)):
-            if shared is not None and lens is not None and len(lens) != problem.batch:
+            if lens is not None and (len(lens) < problem.batch or shared is not None and len(lens) != problem.batch):
                 raise ValueError(f"{what}: {problem.batch} sequences expected, got {len(lens)}")
         self.problem = problem
         self._q = np.ascontiguousarray(q_lens, dtype=np.int32)
@@ -310,8 +365,21 @@ class Plan:
             fn = lib().pkv_plan_decode_dynamic if dynamic else lib().pkv_plan
             _check(fn(*lens, int(num_sms), ctypes.byref(h), ctypes.byref(ws)))
         self.handle = h
+        self._shares = None if shared is not None else False  # tiles over a shared prefix (None: not looked at)
         self.workspace_bytes = int(ws.value)
         self.total_q = int(self._q[:problem.batch].sum())
+        self.total_new = 0 if self._n is None else int(self._n[:problem.batch].sum())
+
+    def rows(self, args: FwdArgs) -> int:
+        """Rows of q, out and lse in a call of this plan (q_rows where the caller places them, which the library
+        refuses if the plan shares a prefix)."""
+        if args.q_rows <= 0:
+            return self.total_q
+        if self._shares is None:
+            import numpy as np
+            seq = np.repeat(np.arange(self.problem.batch), self._q[:self.problem.batch])
+            self._shares = any(seq[it["q_row0"]] != seq[it["q_row0"] + it["n_q"] - 1] for it in self.items())
+        return self.total_q if self._shares else args.q_rows
 
     def stats(self) -> dict:
         s = PlanStats()
@@ -373,6 +441,7 @@ def plan_shared_prefix(problem: Problem, q_lens, cache_lens, new_lens=None, *, g
 
 
 def attn_varlen_kvcache_fwd(problem: Problem, args: FwdArgs, plan_: Plan, workspace, stream=None) -> None:
+    _check_rows(problem, args, plan_.rows(args), plan_.total_new)
     _check(lib().pkv_attn_varlen_kvcache_fwd(ctypes.byref(problem), ctypes.byref(args), plan_.handle,
                                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                              _stream_handle(stream)))
@@ -381,6 +450,7 @@ def attn_varlen_kvcache_fwd(problem: Problem, args: FwdArgs, plan_: Plan, worksp
 def attn_varlen_kvcache_fwd_noalloc(problem: Problem, args: FwdArgs, plan_: Plan, stream=None) -> None:
     """The attention call without a caller workspace (for callers that cannot
     allocate device memory); uses the library's fixed 32 MiB device scratch."""
+    _check_rows(problem, args, plan_.rows(args), plan_.total_new)
     _check(lib().pkv_attn_varlen_kvcache_fwd_noalloc(ctypes.byref(problem), ctypes.byref(args), plan_.handle,
                                                      _stream_handle(stream)))
 
@@ -393,6 +463,7 @@ def get_status_noalloc(stream=None) -> int:
 
 
 def kv_append(problem: Problem, args: FwdArgs, total_new: int, device_status=None, stream=None) -> None:
+    _check_rows(problem, args, 0, total_new)
     _check(lib().pkv_kv_append(ctypes.byref(problem), ctypes.byref(args), int(total_new), _ptr(device_status),
                                _stream_handle(stream)))
 
@@ -400,6 +471,7 @@ def kv_append(problem: Problem, args: FwdArgs, total_new: int, device_status=Non
 def qk_norm_rope(args: QkArgs, spec: RopeSpec, device_status=None, stream=None) -> None:
     """Norm of every head of q and k and the rotation by each token's position, in one pass."""
     _check_weights(getattr(spec, "weight_dim", None), args.head_dim)
+    _check_status_words(device_status)
     _check(lib().pkv_qk_norm_rope(ctypes.byref(args), ctypes.byref(spec), _ptr(device_status),
                                   _stream_handle(stream)))
 
@@ -408,6 +480,8 @@ def rope_kv_append(problem: Problem, args: FwdArgs, rope: RopeAppendArgs, total_
                    device_status=None, stream=None) -> None:
     """``kv_append`` with the norm and rotation on the way into the cache, and of the queries into rope's q_out."""
     _check_rope(problem, rope, total_q)
+    _check_rows(problem, args, total_q if rope.q_out else 0, total_new, bf16=True)
+    _check_status_words(device_status)
     _check(lib().pkv_rope_kv_append(ctypes.byref(problem), ctypes.byref(args), ctypes.byref(rope), int(total_q),
                                     int(total_new), _ptr(device_status), _stream_handle(stream)))
 
@@ -416,6 +490,7 @@ def rope_attn_varlen_kvcache_fwd(problem: Problem, args: FwdArgs, rope: RopeAppe
                                  stream=None) -> None:
     """The attention call with ``rope_kv_append`` in place of its append."""
     _check_rope(problem, rope, plan_.total_q)
+    _check_rows(problem, args, plan_.total_q, plan_.total_new, bf16=True)
     _check(lib().pkv_rope_attn_varlen_kvcache_fwd(ctypes.byref(problem), ctypes.byref(args), ctypes.byref(rope),
                                                   plan_.handle, workspace.data_ptr(),
                                                   workspace.numel() * workspace.element_size(),
