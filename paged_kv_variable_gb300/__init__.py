@@ -178,8 +178,10 @@ def make_problem(*, batch, num_heads_q, num_heads_kv, head_dim, page_size, cache
 def make_args(*, q, out, cu_seqlens_q, max_seqlen_q, k_cache, v_cache, cache_seqlens, lse=None, k_new=None,
               v_new=None, cu_seqlens_knew=None, block_table=None, k_scale=None, v_scale=None,
               page_indptr=None, q_scale=None, q_rows=0) -> FwdArgs:
-    """Pointers and element strides of torch tensors laid out as in pkv.h."""
+    """Pointers and element strides of torch tensors laid out as in pkv.h (which the struct keeps alive)."""
     a = FwdArgs()
+    a.keep = (q, out, cu_seqlens_q, k_cache, v_cache, cache_seqlens, lse, k_new, v_new, cu_seqlens_knew, block_table,
+              k_scale, v_scale, page_indptr, q_scale)
     _same_layout(k_new, v_new, "k_new", "v_new")
     _same_layout(k_cache, v_cache, "k_cache", "v_cache")
     # what the calls compare with the problem and the counts of tokens, of each
@@ -262,8 +264,10 @@ def _need(t, what: str, dtypes: tuple, ndim: int) -> None:
 def make_rope_spec(*, cos_sin=None, interleaved=False, eps=1e-6, q_weight=None, k_weight=None) -> RopeSpec:
     """How rows are normed and rotated.  cos_sin: (positions, rot_dim) fp32, the
     rot_dim/2 cosines and then sines of each position (None: no rotation);
-    q_weight / k_weight: (head_dim,) bf16 RMS norm weights (None: no norm)."""
+    q_weight / k_weight: (head_dim,) bf16 RMS norm weights (None: no norm).  The
+    spec keeps the tensors alive."""
     r = RopeSpec(interleaved=int(bool(interleaved)), eps=eps, q_weight=_ptr(q_weight), k_weight=_ptr(k_weight))
+    r.keep = (cos_sin, q_weight, k_weight)
     r.weight_dim = None  # head_dim that the weights are made for
     for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
@@ -281,10 +285,11 @@ def make_rope_spec(*, cos_sin=None, interleaved=False, eps=1e-6, q_weight=None, 
 
 def make_qk_args(*, q=None, k=None, positions=None, q_out=None, k_out=None) -> QkArgs:
     """Tensors of ``qk_norm_rope``: q (T, Hq, D) and / or k (T, Hkv, D) bf16, int32
-    positions (T,), and where the results go (None: in place)."""
+    positions (T,), and where the results go (None: in place).  The struct keeps the tensors alive."""
     if q is None and k is None:
         raise ValueError("q or k must be given")
     a = QkArgs()
+    a.keep = (q, k, positions, q_out, k_out)
     t = q if q is not None else k
     a.num_tokens, a.head_dim = t.shape[0], t.shape[-1]
     if positions is not None:
@@ -315,8 +320,9 @@ def make_qk_args(*, q=None, k=None, positions=None, q_out=None, k_out=None) -> Q
 
 def make_rope_append_args(*, spec: RopeSpec, q_out=None) -> RopeAppendArgs:
     """The transform of ``rope_kv_append`` and where its queries go (None: the
-    queries are left alone)."""
+    queries are left alone).  The struct keeps q_out and the spec's tensors alive."""
     r = RopeAppendArgs(spec=spec)
+    r.keep = (getattr(spec, "keep", None), q_out)
     r.weight_dim, r.q_shape = getattr(spec, "weight_dim", None), None
     if q_out is not None:
         _need(q_out, "q_out", ("bfloat16",), 3)

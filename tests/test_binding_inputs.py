@@ -136,3 +136,35 @@ def test_status_words(pkv):
     with pytest.raises(ValueError):
         pkv.qk_norm_rope(pkv.make_qk_args(q=_Fake((4, 4, 64)), positions=_Fake((4,), "int32")), spec,
                          device_status=one, stream=0)
+
+
+def test_structs_keep_their_tensors(pkv):
+    """A table, weight or scale made in the call lives as long as the struct that holds its address."""
+    import gc
+    import weakref
+    alive = {}
+
+    def new(what, *shape, dtype="bfloat16"):
+        t = _Fake(shape, dtype)
+        alive[what] = weakref.ref(t)
+        return t
+
+    spec = pkv.make_rope_spec(cos_sin=new("table", 64, 64, dtype="float32"), q_weight=new("q_weight", 64),
+                              k_weight=new("k_weight", 64))
+    rope = pkv.make_rope_append_args(spec=spec, q_out=new("q_out", 4, 4, 64))
+    del spec
+    qk = pkv.make_qk_args(q=new("q", 4, 4, 64), k=new("k", 4, 2, 64), positions=new("pos", 4, dtype="int32"),
+                          q_out=new("qo", 4, 4, 64), k_out=new("ko", 4, 2, 64))
+    args = pkv.make_args(q=new("aq", 4, 4, 64), out=new("out", 4, 4, 64), lse=new("lse", 4, 4, dtype="float32"),
+                         cu_seqlens_q=new("cu", 3, dtype="int32"), max_seqlen_q=3,
+                         k_cache=new("kc", 8, 16, 2, 64), v_cache=new("vc", 8, 16, 2, 64),
+                         cache_seqlens=new("lens", 2, dtype="int32"), k_new=new("kn", 4, 2, 64),
+                         v_new=new("vn", 4, 2, 64), cu_seqlens_knew=new("cun", 3, dtype="int32"),
+                         block_table=new("bt", 2, 4, dtype="int32"), k_scale=new("ks", 1, dtype="float32"),
+                         v_scale=new("vs", 1, dtype="float32"), page_indptr=new("pi", 3, dtype="int32"),
+                         q_scale=new("qs", 1, dtype="float32"))
+    gc.collect()
+    assert [w for w, r in alive.items() if r() is None] == []
+    del rope, qk, args
+    gc.collect()
+    assert [w for w, r in alive.items() if r() is not None] == []
