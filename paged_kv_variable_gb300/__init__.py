@@ -160,9 +160,10 @@ def _ptr(t) -> Optional[int]:
 
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
-        # (torch's own raw query: the current_stream() object costs 3 us a call on the host)
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # (torch's own raw query, where this torch has it: the current_stream() object costs 3 us a call on the host)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

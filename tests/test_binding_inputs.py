@@ -168,3 +168,15 @@ def test_structs_keep_their_tensors(pkv):
     del rope, qk, args
     gc.collect()
     assert [w for w, r in alive.items() if r() is not None] == []
+
+
+def test_current_stream_with_and_without_the_raw_query(pkv, monkeypatch):
+    import types
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device, raising=False)
+    assert pkv._stream_handle(None) == 103
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert pkv._stream_handle(None) == 77
+    assert pkv._stream_handle(5) == 5 and pkv._stream_handle(types.SimpleNamespace(cuda_stream=9)) == 9
