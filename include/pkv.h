@@ -229,9 +229,12 @@ pkv_status pkv_plan_decode_dynamic(const pkv_problem* problem, const int32_t* h_
  * says that it pays (not for a few sequences on a short prefix); 1: always.
  * dynamic = 0: lengths as in pkv_plan; 1: as in pkv_plan_decode_dynamic
  * (h_cache_lens are bounds, the prefixes are fixed; a call whose
- * cache_seqlens[b] is below its prefix records PKV_ERR_PLAN_MISMATCH).
+ * cache_seqlens[b] is below its prefix records PKV_ERR_PLAN_MISMATCH, whether or
+ * not the prefix is shared in the end).
  * A contiguous cache (page_size 0) stores a copy of the prefix per sequence:
- * PKV_ERR_UNSUPPORTED, and so is a call with q_rows > 0.  Pure host code.
+ * PKV_ERR_UNSUPPORTED.  So is a call with q_rows > 0 of a plan that shares a
+ * prefix; one that ends up sharing none takes it as any other plan.  Pure host
+ * code.
  */
 pkv_status pkv_plan_shared_prefix(const pkv_problem* problem, const int32_t* h_q_lens,
                                   const int32_t* h_cache_lens, const int32_t* h_new_lens,

@@ -566,10 +566,6 @@ pkv_status run_call(const pkv_problem* problem, const pkv_fwd_args* args, const 
     cp.lse = p.lse;
     cp.total_q = p.total_q;
     cp.G = p.G;
-    if (plan->shared && plan->dynamic) cp.plan_min = reinterpret_cast<const int32_t*>(ws + plan->layout.plan_min);
-    cp.cache_seqlens = p.cache_seqlens;
-    cp.batch = p.batch;
-    cp.status = p.status;
     e = plan->row_combine
             ? launch_combine_shared(cp, plan->num_combine, plan->max_combine_rows, plan->max_combine_parts, pr.head_dim,
                                     overlap && !g_ev_stop, s)

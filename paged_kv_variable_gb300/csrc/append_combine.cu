@@ -169,13 +169,6 @@ __global__ void __launch_bounds__(32 * kSharedCombineWarps) combine_shared_kerne
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = ci.n_q * ci.nh, parts = ci.p_nsplit + ci.nsplit;
   grid_dep_wait();  // the partials come from the attention kernel launched just before
-  if (p.plan_min != nullptr && blockIdx.x == 0 && blockIdx.y == 0) {
-    // (the attention kernel checks the lengths against their bounds)
-    for (int b = threadIdx.x; b < p.batch; b += 32 * kSharedCombineWarps) {
-      const int lc = __ldg(p.cache_seqlens + b);
-      if (lc < __ldg(p.plan_min + b)) record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
-    }
-  }
   const int row = SPLIT ? (int)blockIdx.y : blockIdx.y * kSharedCombineWarps + warp;
   if (row >= rows) return;  // (SPLIT: the whole block)
   const int w0 = SPLIT ? warp : 0;  // this warp's parts: w0, w0 + W, ...

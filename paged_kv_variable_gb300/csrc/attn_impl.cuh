@@ -1960,8 +1960,10 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
   const bool mma_consumer = ctid < 32 * L::kDecWarps;  // the decode consumer warps
   if (blockIdx.x == 0 && mma_consumer) {
     for (int b = ctid; b < p.batch; b += 32 * L::kDecWarps) {
-      const int lc = __ldg(p.cache_seqlens + b), planned = __ldg(p.plan_lc + b);
-      if (p.dynamic ? (lc < 0 || lc > planned) : lc != planned) record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
+      // (the planned length itself; of a dynamic plan its bound, and 0 or the prefix of the sequence's group)
+      const int lc = __ldg(p.cache_seqlens + b);
+      if (lc > __ldg(p.plan_lc + b) || lc < __ldg(p.plan_lc + p.batch + b))
+        record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
     }
   }
   const float kscale = FP8 ? __ldg(p.k_scale) : 1.f;

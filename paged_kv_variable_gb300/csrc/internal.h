@@ -105,8 +105,7 @@ struct WorkspaceLayout {
   size_t items;         // WorkItem[num_items], grouped by CTA
   size_t cta_begin;     // int32[num_ctas + 1]
   size_t combine;       // CombineItem[num_combine]
-  size_t plan_lc;       // int32[B] cache lengths the plan was made for
-  size_t plan_min;      // int32[B] (shared-prefix plans) least cache lengths: the prefixes
+  size_t plan_lc;       // int32[2 B] cache lengths the plan was made for: the largest, then the least
   size_t partial_o;     // float[num_slots * kDecodeRows * D]
   size_t partial_lse;   // float[num_slots * kDecodeRows] (log2 domain)
   size_t total;

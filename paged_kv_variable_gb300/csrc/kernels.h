@@ -62,11 +62,6 @@ struct CombineParams {
   float* lse;
   int32_t total_q;
   int32_t G;
-  // plans with shared prefixes and current lengths: [batch] least lengths to check
-  const int32_t* plan_min;  // nullable
-  const int32_t* cache_seqlens;
-  int32_t batch;
-  int* status;
 };
 
 struct AttnParams {
@@ -100,7 +95,7 @@ struct AttnParams {
   float* partial_lse;
   int* status;
   const int32_t* cache_seqlens;
-  const int32_t* plan_lc;
+  const int32_t* plan_lc;  // [2 * batch] largest, then least cache lengths of a call
   int32_t batch;
   int32_t dynamic;     // plan_lc holds bounds; the cache lengths come from cache_seqlens
   int32_t dep_first;   // launched while the call's rotating append drains: wait for it before anything is read

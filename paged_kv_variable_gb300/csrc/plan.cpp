@@ -723,9 +723,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   L.combine = off;
   off = align_up(off + sizeof(CombineItem) * (size_t)std::max<size_t>(1, combines.size()), 256);
   L.plan_lc = off;
-  off = align_up(off + sizeof(int32_t) * (size_t)std::max(1, B), 256);
-  L.plan_min = off;
-  if (!runs.empty()) off = align_up(off + sizeof(int32_t) * (size_t)std::max(1, B), 256);
+  off = align_up(off + 2 * sizeof(int32_t) * (size_t)std::max(1, B), 256);
   size_t image_bytes = off;
   L.partial_o = off;
   off = align_up(off + sizeof(float) * (size_t)num_slots * kDecodeRows * D, 256);
@@ -786,8 +784,10 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   }
   if (!combines.empty()) memcpy(plan->image + L.combine, combines.data(), combines.size() * sizeof(CombineItem));
   int32_t* lc = (int32_t*)(plan->image + L.plan_lc);
-  for (int b = 0; b < B; ++b) lc[b] = h_cache_lens[b];
-  if (plan->shared) memcpy(plan->image + L.plan_min, least.data(), sizeof(int32_t) * (size_t)B);
+  for (int b = 0; b < B; ++b) {
+    lc[b] = h_cache_lens[b];
+    lc[B + b] = dynamic ? least[b] : h_cache_lens[b];  // (dynamic: 0, or the prefix of the sequence's group)
+  }
 
   *out_plan = plan;
   *out_workspace_bytes = L.total;

@@ -623,3 +623,29 @@ def test_rotated_append_and_shared_attention_together(pkv, gpu, fp8):
         got = c.kc[torch.from_numpy(c.pages[seq, pos // 16].astype(np.int64)).cuda(), torch.from_numpy(pos % 16).cuda()]
         close_bf16(got, want_k, mag)
     c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
+def test_lengths_below_the_prefix_are_reported_where_nothing_is_shared(pkv, gpu, wide):
+    """A dynamic plan checks its prefixes whether or not they pay: sharing declined by the time model, or never
+    possible (head groups of more than 64)."""
+    torch = gpu
+    B = 3
+    kw = dict(hq=200, hkv=1) if wide else dict(hq=8, hkv=2)
+    c = Shared(pkv, torch, 31, starts=[0, B], prefix=[256], own=[5, 40, 17], q=[1] * B, new=[1] * B, dynamic=True,
+               bound=3, shares=not wide, **kw)
+    c.plan = pkv.plan_shared_prefix(c.problem, c.q_lens, c.cache + 3, c.new, group_starts=[0, B], prefix_lens=[256],
+                                    dynamic=True)
+    plain = pkv.plan_decode_dynamic(c.problem, c.q_lens, c.cache + 3, c.new)
+    assert c.plan.items() == plain.items() and c.plan.stats()["num_split_units"] == 0
+    c.ws = pkv.workspace_tensor(c.plan.workspace_bytes)
+    c.plan.upload(c.ws)
+    assert c.run() == 0
+    c.check()
+    # (-1: the append, which comes first, reports the position)
+    for at, lc, status in ((1, 255, 7), (1, 256, 0), (2, -1, 6), (0, int(c.cache[0]) + 4, 7), (0, int(c.cache[0]), 0)):
+        lens = c.cache.copy()
+        lens[at] = lc
+        c.lens.copy_(H.i32(lens))
+        assert c.run() == status
