@@ -300,6 +300,7 @@ extern "C" pkv_status pkv_kv_append(const pkv_problem* problem, const pkv_fwd_ar
   st = validate_new_args(*problem, args);
   if (st != PKV_OK) return st;
   AppendParams ap = append_params(*problem, args, total_new, reinterpret_cast<int*>(device_status));
+  ap.status_code_only = 1;
   cudaError_t e = launch_kv_append(ap, problem->head_dim, problem->cache_dtype == PKV_FP8_E4M3,
                                    static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");

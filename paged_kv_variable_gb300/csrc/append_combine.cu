@@ -36,9 +36,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
     if (__ldg(p.cu_knew + mid) <= t) lo = mid; else hi = mid;
   }
   const int b = lo;
+  auto report = [&](int at) {
+    if (p.status_code_only) record_code(p.status, PKV_ERR_DEVICE_BOUNDS);
+    else record_status(p.status, PKV_ERR_DEVICE_BOUNDS, b, at);
+  };
   const int pos = __ldg(p.cache_seqlens + b) + (t - __ldg(p.cu_knew + b));
   if (pos < 0 || pos >= p.capacity) {
-    if (lane == 0) record_status(p.status, PKV_ERR_DEVICE_BOUNDS, b, pos);
+    if (lane == 0) report(pos);
     return;
   }
   int64_t dst;
@@ -48,7 +52,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
     const int pi = pos / p.page_size;
     const int page = (npages >= 0 && pi >= npages) ? -1 : __ldg(pages + pi);
     if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) record_status(p.status, PKV_ERR_DEVICE_BOUNDS, b, page);
+      if (lane == 0) report(page);
       return;
     }
     dst = (int64_t)page * p.c_stride_page + (int64_t)(pos % p.page_size) * p.c_stride_tok;

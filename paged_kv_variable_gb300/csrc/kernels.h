@@ -30,6 +30,7 @@ struct AppendParams {
   const float* k_scale;
   const float* v_scale;
   int* status;
+  int status_code_only;  // status is one word (the caller's own); else three: the code and two details
 };
 
 // Norm + rotation of query and key rows (pkv_rope_spec), alone or on the way

@@ -307,13 +307,19 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
 }
 
 // ---------------------------------------------------------------- status word
-// Records the first device-side error of a call (never traps).
+// Records the first device-side error of a call (never traps): the code and two
+// details.
 __device__ __forceinline__ void record_status(int* status, int code, int info0, int info1) {
   if (status == nullptr) return;
   if (atomicCAS(status, 0, code) == 0) {
     status[1] = info0;
     status[2] = info1;
   }
+}
+
+// The code alone, into a status of one word.
+__device__ __forceinline__ void record_code(int* status, int code) {
+  if (status != nullptr) atomicCAS(status, 0, code);
 }
 
 }  // namespace pkv
