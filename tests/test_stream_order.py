@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 
 from tests import harness as H
-from tests.test_rope import AppendCase
+from tests.test_rope import AppendCase, bf16
 from tests.test_shared_prefix import Shared
 
 pytestmark = pytest.mark.gpu
@@ -137,3 +137,73 @@ def test_shared_prefixes(pkv, kw):
     args = c.args()
     first, rest = edges_of(lambda s: pkv.attn_varlen_kvcache_fwd(c.problem, args, c.plan, c.ws, stream=s))
     assert first == [0] and rest
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("tokens", [2, 700])
+@pytest.mark.parametrize("form", ["rotating", "plain", "call"])
+def test_keys_and_values_written_just_before_and_read_just_after(pkv, form, tokens, fp8):
+    """The append reads the queries, keys, values and lengths that the kernel before it
+    wrote, and the kernel after it the cache: eager and in a graph, step after step."""
+    import torch
+    c = AppendCase(pkv, torch, 11, d=128, page=16, fp8=fp8, new=[tokens, 1, tokens // 2], cached=[20, 0, 33], far=900)
+    rng = np.random.default_rng(12)
+    inputs = [[bf16(torch, rng, *t.shape) for t in (c.q, c.k, c.v)] + [H.i32(np.array(lens, np.int32))]
+              for lens in ([20, 0, 33], [7, 30, 2], [16, 1, 0])]
+    empty = [c.kc.clone(), c.vc.clone()]
+    out = torch.zeros_like(c.q_out)
+    args = c.args(out=out)
+    plans = []
+    for lens in ([20, 0, 33], [7, 30, 2], [16, 1, 0]):
+        plan = pkv.plan(c.problem, c.q_lens, lens, c.new)
+        plans.append((plan, pkv.workspace_tensor(plan.workspace_bytes)))
+        plan.upload(plans[-1][1])
+    busy = torch.randn(1 << 24, device="cuda")
+
+    def step(i, got):
+        busy.mul_(1.0001)
+        for cache, e in zip((c.kc, c.vc), empty):
+            cache.copy_(e)
+        for t, x in zip((c.q, c.k, c.v, c.lens), inputs[i % 3]):
+            t.copy_(x)
+        if form == "plain":
+            pkv.kv_append(c.problem, args, c.tn)
+        elif form == "rotating":
+            pkv.rope_kv_append(c.problem, args, c.rope, c.tq, c.tn)
+        else:
+            plan, ws = plans[i % 3]
+            pkv.rope_attn_varlen_kvcache_fwd(c.problem, args, c.rope, plan, ws)
+        for g, x in zip(got, (c.kc, c.vc, c.q_out, out)):
+            g.copy_(x)
+
+    def buffers():
+        return [torch.zeros_like(x) for x in (c.kc, c.vc, c.q_out, out)]
+
+    def same(a, b):
+        return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+    c.q_out.zero_()
+    want = []
+    for i in range(3):
+        want.append(buffers())
+        step(i, want[-1])
+        torch.cuda.synchronize()
+        if form != "plain":                     # (against 64 bits)
+            c.cached = inputs[i][3].cpu().numpy()
+            c.check(*(H.to_numpy_bits(e).copy() for e in empty))
+    assert not any(same(want[i], want[j]) for i, j in ((0, 1), (1, 2), (0, 2)))
+    got = [buffers() for _ in range(9)]
+    for i, g in enumerate(got):
+        step(i, g)
+    torch.cuda.synchronize()
+    assert all(same(g, want[i % 3]) for i, g in enumerate(got))
+    for g in got:
+        for x in g:
+            x.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i, g in enumerate(got):
+            step(i, g)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(same(g, want[i % 3]) for i, g in enumerate(got))
