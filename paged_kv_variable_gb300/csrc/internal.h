@@ -69,8 +69,9 @@ struct WorkItem {
   int32_t n_q;       // query tokens in the tile
   int32_t lq;        // query length of the sequence
   int32_t lk;        // attended keys of the sequence (cache + new)
-  int32_t kv_begin;  // key range of this item, kv_begin a multiple of kKvTile
-  int32_t kv_end;
+  int32_t kv_begin;  // key range of this item: kv_begin is a multiple of kKvTile past the end of the
+  int32_t kv_end;    // sequence's shared prefix (whole pages; 0 without one), so of the cache's box rows,
+                     // which divide a tile and a page, but not of a tile
   int32_t kind;      // ItemKind
   int32_t partial;   // -1: write the final output; else the first partial slot (16 rows each)
   int32_t h0;        // first query head of the group in this tile
