@@ -188,7 +188,10 @@ def make_args(*, q, out, cu_seqlens_q, max_seqlen_q, k_cache, v_cache, cache_seq
     # what the calls compare with the problem and the counts of tokens, of each
     # tensor whose address the struct still holds by then
     a.given = {what: (t.data_ptr(), tuple(t.shape), str(getattr(t, "dtype", "bfloat16")).removeprefix("torch."))
-               for what, t in (("q", q), ("out", out), ("lse", lse), ("k_new", k_new), ("v_new", v_new))
+               for what, t in (("q", q), ("out", out), ("lse", lse), ("k_new", k_new), ("v_new", v_new),
+                               ("k_cache", k_cache), ("cu_seqlens_q", cu_seqlens_q), ("cache_seqlens", cache_seqlens),
+                               ("cu_seqlens_knew", cu_seqlens_knew), ("block_table", block_table),
+                               ("page_indptr", page_indptr))
                if t is not None}
     a.checked = None  # the last call that they were found to serve
     if q is not None:
@@ -226,13 +229,16 @@ def _same_layout(x, y, what_x: str, what_y: str) -> None:
 def _check_rows(problem: Problem, args: FwdArgs, total_q: int, total_new: int, bf16: bool = False) -> None:
     """The tensors of make_args against the rows that the call reads and writes:
     q and out (rows, Hq, D), k_new and v_new (rows, Hkv, D), lse (Hq, rows), with
-    at least so many rows and heads.  Structs that were not made by make_args, and
-    addresses put in since, are taken as they are."""
+    at least so many rows and heads, and the caches, offsets and page tables with the
+    problem.  Structs that were not made by make_args, and addresses put in since,
+    are taken as they are."""
     given = getattr(args, "given", None)
-    call = (total_q, total_new, problem.num_heads_q, problem.num_heads_kv, problem.head_dim, bf16)
-    if given is None or call == args.checked:
+    if given is None:
         return
-    d = problem.head_dim
+    call = (total_q, total_new, bf16, bytes(problem))
+    if call == args.checked:
+        return
+    d, batch = problem.head_dim, problem.batch
     for what, rows, heads in (("q", total_q, problem.num_heads_q), ("out", total_q, problem.num_heads_q),
                               ("k_new", total_new, problem.num_heads_kv), ("v_new", total_new, problem.num_heads_kv)):
         if rows > 0 and what in given:
@@ -246,6 +252,21 @@ def _check_rows(problem: Problem, args: FwdArgs, total_q: int, total_new: int, b
         ptr, shape, _ = given["lse"]
         if math.prod(shape) < problem.num_heads_q * total_q and args.lse == ptr:
             raise PkvInputError(f"lse {shape}: ({problem.num_heads_q}, {total_q}) expected")
+    for what, least in (("cu_seqlens_q", batch + 1 if total_q > 0 else 0), ("cache_seqlens", batch),
+                        ("cu_seqlens_knew", batch + 1 if total_new > 0 else 0), ("page_indptr", batch + 1)):
+        if what in given:
+            ptr, shape, _ = given[what]
+            if math.prod(shape) < least and getattr(args, what) == ptr:
+                raise PkvInputError(f"{what} {shape}: {least} values expected")
+    tokens = problem.page_size or problem.cache_capacity
+    ptr, shape, _ = given["k_cache"]
+    if (len(shape) != 4 or shape[0] < problem.num_pages or shape[1] < tokens or shape[2] < problem.num_heads_kv
+            or shape[3] != d) and args.k_cache == ptr:
+        raise PkvInputError(f"k_cache {shape}: ({problem.num_pages}, {tokens}, {problem.num_heads_kv}, {d}) expected")
+    if "block_table" in given and "page_indptr" not in given:  # (the library looks at the stride of its rows)
+        ptr, shape, _ = given["block_table"]
+        if shape[0] < batch and args.block_table == ptr:
+            raise PkvInputError(f"block_table {shape}: {batch} rows expected")
     args.checked = call
 
 

@@ -109,6 +109,25 @@ def test_pairs_share_shape_and_strides(pkv):
     make(pkv, k_new=_Fake((1, 2, 64)), v_new=_Fake((1, 2, 64), strides=[7, 64, 1]))
 
 
+@pytest.mark.parametrize("over", [
+    dict(cu_seqlens_q=_Fake((2,), "int32")), dict(cache_seqlens=_Fake((1,), "int32")),
+    dict(cu_seqlens_knew=_Fake((2,), "int32")), dict(block_table=_Fake((1, 4), "int32")),
+    dict(block_table=_Fake((8,), "int32"), page_indptr=_Fake((2,), "int32")),
+    *(dict(k_cache=_Fake(s), v_cache=_Fake(s)) for s in ((7, 16, 2, 64), (8, 8, 2, 64), (8, 16, 1, 64), (8, 16, 2, 32)))])
+def test_offsets_tables_and_caches_too_small(pkv, over):
+    prob, args, pl = make(pkv, **over)
+    for call in calls(pkv, prob, args, pl):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_a_ragged_page_list_reaches_the_library(pkv):
+    for call in calls(pkv, *make(pkv, block_table=_Fake((5,), "int32"), page_indptr=_Fake((3,), "int32"))):
+        with pytest.raises(pkv.PkvError) as e:
+            call()
+        assert "workspace" in pkv.last_error() and not isinstance(e.value, ValueError)
+
+
 def test_an_address_put_in_later_is_taken_as_it_is(pkv):
     prob, args, pl = make(pkv, q=_Fake((3, 4, 64)))
     args.q = 1 << 21
