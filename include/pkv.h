@@ -340,8 +340,8 @@ pkv_status pkv_get_status_noalloc(void* stream, int32_t* device_status);
  * logical position cache_seqlens[b] + t: page block_table[b][pos / P], slot
  * pos % P (or row pos of batch b for a contiguous cache).  bf16 caches get the
  * bits unchanged; fp8 caches get e4m3_rn_satfinite(fp32(x) * fp32(1/scale)),
- * bit-exact.  total_new = sum of new lengths (host int).  device_status (one word):
- * nullable device int32 that receives the first device error code.
+ * bit-exact.  total_new = sum of new lengths (host int).  device_status:
+ * nullable device int32 (one word) that receives the first device error code.
  */
 pkv_status pkv_kv_append(const pkv_problem* problem, const pkv_fwd_args* args,
                          int32_t total_new, int32_t* device_status, void* stream);
