@@ -241,8 +241,19 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherParams 
   const int b = seq.b;
   if (p.lens != nullptr && seq.row(p.cu_rows, t) >= __ldg(p.lens + b)) return;
   const int pos = seq.start(p.starts) + seq.row(p.cu_rows, t);
+  const int half = p.head_dim / 32;  // blocks between a thread's two
+  const int64_t dst = (int64_t)t * p.o_stride_tok + (int64_t)h * p.o_stride_head + part * 16;
+  // a position or page out of range: nothing is written or, of copies that an attention reads
+  // (a workspace holds rows of the call before), zeros, as the tiles straight over a cache have
   auto report = [&](int at) {
     if (part == 0) record_status(p.status, PKV_ERR_DEVICE_BOUNDS, b, at);
+    if (p.lens == nullptr) return;
+    const uint32_t none[8] = {};
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+      store16(p.k_out + dst + k * half * 16, wide & 2, none);
+      store16(p.v_out + dst + k * half * 16, wide & 2, none);
+    }
   };
   if (pos < 0 || pos >= p.capacity) return report(pos);
   int64_t page = b;
@@ -257,12 +268,10 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherParams 
     slot = pos - pi * p.page_size;
   }
   constexpr int kBytes = DT == PKV_BF16 ? 32 : DT == PKV_FP8_E4M3 ? 16 : 8;  // of a block of 16 dims
-  const int half = p.head_dim / 32;                                         // blocks between a thread's two
   const int64_t at = (page * p.c_stride_page + (int64_t)slot * p.c_stride_tok + (int64_t)h * p.c_stride_head) *
                          (DT == PKV_BF16 ? 2 : 1) +
                      part * kBytes;
   const int64_t sat = page * p.sf.stride_page + (int64_t)slot * p.sf.stride_tok + (int64_t)h * p.sf.stride_head + part;
-  const int64_t dst = (int64_t)t * p.o_stride_tok + (int64_t)h * p.o_stride_head + part * 16;
   uint32_t w[2][kBlocks][8];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {

@@ -77,7 +77,8 @@ struct GatherParams {
   Fp4Scales sf;
   const float* k_scale;  // nullable: 1
   const float* v_scale;
-  const int32_t* lens;   // nullable: [batch] rows of a sequence past these are left out
+  const int32_t* lens;   // nullable (copies that an attention reads, k_out and v_out given): [batch] rows of a
+                         // sequence past these are left out, those of a page out of range zeros
   const int32_t* cache_seqlens;  // (with lens) compared with the lengths of the plan
   const int32_t* plan_lc;
   int* status;
