@@ -398,6 +398,8 @@ typedef struct {
   int64_t stride_seq, stride_head;
   int32_t last_queries;    /* 0: every query row; > 0: the last so many of each sequence */
   int32_t max_seqlen_k;    /* bound on the keys of a sequence (0: cache_capacity) */
+  int32_t max_total_q;     /* 0, or the query rows that q and lse have room for:
+                              a cu_seqlens_q[B] beyond is refused on the device    */
 } pkv_weights_args;
 
 /*
@@ -410,9 +412,10 @@ typedef struct {
  * the group.  A row with lse -inf adds nothing.  Keys past the sequence keep what
  * scores holds there.  Sums are fp32, in a fixed order.  args->max_seqlen_q bounds
  * the query lengths.  q_rows and q_scale must be 0 / NULL.  A sequence longer than
- * max_seqlen_k or a query run longer than max_seqlen_q records
- * PKV_ERR_PLAN_MISMATCH in device_status (nullable device int32[3]) and its scores
- * are not written; a bad page PKV_ERR_DEVICE_BOUNDS, and its keys' are not.
+ * max_seqlen_k, a query run longer than max_seqlen_q, or one that cu_seqlens_q places
+ * outside of its cu_seqlens_q[B] rows, or all of them if those are more than
+ * max_total_q, record PKV_ERR_PLAN_MISMATCH in device_status (nullable device int32[3])
+ * and their scores are not written; a bad page PKV_ERR_DEVICE_BOUNDS, and its keys' are not.
  */
 pkv_status pkv_attn_weights(const pkv_problem* problem, const pkv_fwd_args* args, const pkv_weights_args* weights,
                             int32_t* device_status, void* stream);

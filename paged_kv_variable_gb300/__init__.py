@@ -75,7 +75,8 @@ class GatherArgs(ctypes.Structure):
 
 class WeightsArgs(ctypes.Structure):
     _fields_ = [("scores", ctypes.c_void_p), ("scores_in", ctypes.c_void_p), ("stride_seq", ctypes.c_int64),
-                ("stride_head", ctypes.c_int64), ("last_queries", ctypes.c_int32), ("max_seqlen_k", ctypes.c_int32)]
+                ("stride_head", ctypes.c_int64), ("last_queries", ctypes.c_int32), ("max_seqlen_k", ctypes.c_int32),
+                ("max_total_q", ctypes.c_int32)]
 
 
 class EvictArgs(ctypes.Structure):
@@ -306,6 +307,35 @@ def _check_rows(problem: Problem, args: FwdArgs, total_q: int, total_new: int, b
         if shape[0] < batch and args.block_table == ptr:
             raise PkvInputError(f"block_table {shape}: {batch} rows expected")
     args.checked = (call, *args.checked[:3])
+
+
+def _query_rows(problem: Problem, args: FwdArgs) -> int:
+    """The tensors that a call reads beside the attention's plan, rows by cu_seqlens_q on the device: q, lse (Hq, rows)
+    and the offsets.  Returns the rows that q and lse have room for (0: not known)."""
+    call = (args.q, args.lse, args.cu_seqlens_q, args.cu_seqlens_knew, args.k_new, bytes(problem))
+    checked, bound = getattr(args, "query_rows", (None, 0))
+    if call == checked:
+        return bound
+    given = {what: t for what, t in getattr(args, "given", {}).items() if getattr(args, what) == t[0]}
+    hq, rows = problem.num_heads_q, []
+    if "q" in given:
+        _, shape, dtype = given["q"]
+        if len(shape) != 3 or shape[1] < hq or shape[2] != problem.head_dim or dtype != "bfloat16":
+            raise PkvInputError(f"q {shape}: bfloat16 (rows, {hq}, {problem.head_dim}) expected")
+        rows.append(shape[0])
+    if "lse" in given:
+        _, shape, dtype = given["lse"]
+        if math.prod(shape) < hq or dtype != "float32":
+            raise PkvInputError(f"lse {shape} {dtype}: float32 ({hq}, rows) expected")
+        rows.append(math.prod(shape) // hq)
+    for what in ("cu_seqlens_q", "cu_seqlens_knew") if args.k_new else ("cu_seqlens_q",):
+        if what in given:
+            _, shape, dtype = given[what]
+            if math.prod(shape) < problem.batch + 1 or dtype != "int32":
+                raise PkvInputError(f"{what} {shape} {dtype}: {problem.batch + 1} int32 expected")
+    bound = min(rows + [(1 << 31) - 1]) if rows else 0
+    args.query_rows = (call, bound)
+    return bound
 
 
 def _check_status_words(device_status) -> None:
@@ -612,10 +642,7 @@ def attn_weights(problem: Problem, args: FwdArgs, weights: WeightsArgs, device_s
     """The attention weight that every cached key received from the queries of a call that has run (its arguments,
     with its lse), summed over the queries and the heads of a group."""
     _check_rows(problem, args, 0, 0)
-    q = getattr(args, "given", {}).get("q")
-    if q is not None and args.q == q[0] and (len(q[1]) != 3 or q[1][1] < problem.num_heads_q
-                                             or q[1][2] != problem.head_dim or q[2] != "bfloat16"):
-        raise PkvInputError(f"q {q[1]}: bfloat16 (rows, {problem.num_heads_q}, {problem.head_dim}) expected")
+    weights.max_total_q = _query_rows(problem, args)
     _check_status_words(device_status)
     _check_scores(problem, weights, weights.max_seqlen_k or problem.cache_capacity)
     _check(lib().pkv_attn_weights(ctypes.byref(problem), ctypes.byref(args), ctypes.byref(weights),

@@ -809,7 +809,8 @@ extern "C" pkv_status pkv_attn_weights(const pkv_problem* problem, const pkv_fwd
     return fail(PKV_ERR_INVALID_ARG, "max_seqlen_k %d: 0 to cache_capacity", w.max_seqlen_k);
   const int32_t most = w.max_seqlen_k > 0 ? w.max_seqlen_k : pr.cache_capacity;
   if (most > kMaxSeqlen) return fail(PKV_ERR_UNSUPPORTED, "max_seqlen_k %d > %d", most, kMaxSeqlen);
-  if (w.last_queries < 0 || args->max_seqlen_q < 0) return fail(PKV_ERR_INVALID_ARG, "last_queries or max_seqlen_q < 0");
+  if (w.last_queries < 0 || args->max_seqlen_q < 0 || w.max_total_q < 0)
+    return fail(PKV_ERR_INVALID_ARG, "last_queries, max_seqlen_q or max_total_q < 0");
   if (args->q_rows != 0) return fail(PKV_ERR_UNSUPPORTED, "attn_weights takes packed query rows (q_rows = 0)");
   if (args->q_scale) return fail(PKV_ERR_UNSUPPORTED, "attn_weights takes no quantised queries (q_scale)");
   if (pr.batch > kMaxGridDim || pr.num_heads_kv > kMaxGridDim)
@@ -857,6 +858,7 @@ extern "C" pkv_status pkv_attn_weights(const pkv_problem* problem, const pkv_fwd
   p.last_queries = w.last_queries;
   p.max_seqlen_k = most;
   p.max_seqlen_q = args->max_seqlen_q;
+  p.max_total_q = w.max_total_q;
   p.causal = pr.causal;
   p.scale_log2 = pr.softmax_scale * 1.4426950408889634f;
   p.status = reinterpret_cast<int*>(device_status);

@@ -153,7 +153,7 @@ struct WeightsParams {
   float* scores;
   const float* scores_in;  // nullable
   int64_t s_stride_seq, s_stride_head;
-  int32_t last_queries, max_seqlen_k, max_seqlen_q, causal;
+  int32_t last_queries, max_seqlen_k, max_seqlen_q, max_total_q, causal;
   float scale_log2;
   int* status;
 };

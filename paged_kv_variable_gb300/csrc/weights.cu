@@ -119,7 +119,9 @@ __device__ __forceinline__ Seq load_seq(const WeightsParams& p, int b, bool repo
   s.total_q = __ldg(p.cu_q + p.batch);
   s.lk = __ldg(p.cache_seqlens + b);
   if (p.cu_knew != nullptr) s.lk += __ldg(p.cu_knew + b + 1) - __ldg(p.cu_knew + b);
-  s.ok = s.lk >= 0 && s.lk <= p.max_seqlen_k && s.lq >= 0 && s.lq <= p.max_seqlen_q;
+  // (lse is (Hq, total_q): rows outside of it, or of q, are never read)
+  s.ok = s.lk >= 0 && s.lk <= p.max_seqlen_k && s.lq >= 0 && s.lq <= p.max_seqlen_q && s.q0 >= 0 &&
+         (int64_t)s.q0 + s.lq <= s.total_q && (p.max_total_q == 0 || s.total_q <= p.max_total_q);
   if (!s.ok && report) record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, s.lk);
   s.first = p.last_queries > 0 ? max(0, s.lq - p.last_queries) : 0;
   s.rows = s.ok ? (s.lq - s.first) * p.G : 0;
