@@ -603,7 +603,7 @@ def kv_gather(problem: Problem, args: FwdArgs, gather: GatherArgs, total_rows: i
         if shape[0] < total_rows or shape[1] < problem.num_heads_kv or shape[2] != problem.head_dim:
             raise PkvInputError(
                 f"k_out / v_out {shape}: ({total_rows}, {problem.num_heads_kv}, {problem.head_dim}) expected")
-        if gather.counts[0] < problem.batch + 1 or (gather.counts[1] or problem.batch) < problem.batch:
+        if gather.counts[0] < problem.batch + 1 or (gather.counts[1] is not None and gather.counts[1] < problem.batch):
             raise PkvInputError(f"cu_rows, starts {gather.counts}: {problem.batch} sequences expected")
     _check(lib().pkv_kv_gather(ctypes.byref(problem), ctypes.byref(args), ctypes.byref(gather), int(total_rows),
                                _ptr(device_status), _stream_handle(stream)))

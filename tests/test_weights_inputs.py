@@ -1,10 +1,11 @@
-"""What attn_weights reads by offsets on the device: tensors with too few values are refused before a launch,
+"""What attn_weights and kv_gather read by offsets on the device: tensors with too few values are refused before a launch,
 rows outside of them by the kernel."""
 import numpy as np
 import pytest
 import torch
 
 from tests import long_cache as LC
+from tests.test_fp4 import make as make_fp4
 from tests.test_rope import _Fake
 from tests.test_weights import S, make
 
@@ -47,6 +48,14 @@ def test_rows_that_the_tensors_hold(pkv, q, lse, rows):
     with pytest.raises(pkv.PkvError, match="aligned"):
         pkv.attn_weights(prob, args, w, stream=0)
     assert w.max_total_q == 0
+
+
+@pytest.mark.parametrize("starts", [0, 1])
+def test_gathers_with_short_starts_are_refused(pkv, starts):
+    prob, args = make_fp4(pkv)
+    g = pkv.make_gather_args(cu_rows=_Fake((3,), "int32"), k_out=_Fake((4, 2, 64)), starts=_Fake((starts,), "int32"))
+    with pytest.raises(pkv.PkvError, match="starts"):
+        pkv.kv_gather(prob, args, g, 4, stream=0)
 
 
 @pytest.mark.gpu
