@@ -189,7 +189,7 @@ typedef struct {
  * two CTAs an SM (the plan's stats report the count).
  * Over an fp4 cache the tiles are of 8, 16 or 32 rows (head_dim 256, 128, 64), a
  * CTA each, whatever the query length; sequences whose many query rows make it
- * worth it are attended by the tensor-core tiles over bf16 copies of their cached
+ * worth it are attended by the tensor-core tiles over 16-bit copies of their cached
  * rows, which the call makes in the workspace: 4 * head_dim bytes a key and kv
  * head, in all at most 4 GiB (a batch that needs more is planned without).  Their
  * cache lengths have to be the plan's.  At most 2^30 keys a sequence.

@@ -574,10 +574,10 @@ pkv_status run_attention(const pkv_problem& pr, const pkv_fwd_args* args, const 
   return PKV_OK;
 }
 
-// The sequences of a 4-bit plan whose queries fill tensor-core tiles: their rows as
-// bf16 (exact: code x block scale has six significant bits; the tensor scales go
-// into the logits' scale and the output) into the workspace, then the attention
-// over those.
+// The sequences of a 4-bit plan whose queries fill tensor-core tiles: their keys as
+// bf16, to meet the queries, and their values as f16, to meet P (both exact: code x
+// block scale has six significant bits; the tensor scales go into the logits' scale
+// and the output), into the workspace, then the attention over those.
 pkv_status run_far(const pkv_problem& pr, const pkv_fwd_args* args, pkv_plan_t plan, unsigned char* ws, cudaStream_t s) {
   const FarLayout& F = plan->far_layout;
   const pkv_plan_s* far = plan->far;

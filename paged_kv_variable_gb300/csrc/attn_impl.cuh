@@ -50,6 +50,7 @@ namespace {
 constexpr int kConsumerWarps = 4;                  // warp-MMA consumers (decode, fp8 prefill): warps 2..5
 constexpr int kConsumerThreads = 32 * kConsumerWarps;
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kPExp = 6.f;  // (copies of a 4-bit cache's rows) P = 2^(logit - max + kPExp)
 // Tensor memory: at D <= 128 (two query tiles per prefill item) query tile q
 // has one S buffer of a tile's keys (fp32) at 256q and its O (D fp32 columns)
 // at 256q + 128; at D = 256 three S buffers [0,64), [64,128), [128,192) of the
@@ -664,11 +665,11 @@ __device__ bool s_issuer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
   return true;
 }
 
-template <int D, bool FP8, bool PF>
+template <int D, bool FP8, bool PF, bool R4>
 __device__ bool pv_issuer(const AttnParams& p, uint8_t* smem, const Bars& B, volatile int* abort_flag, uint32_t tmem,
                           int it0, int it1) {
   using L = Layout<D, FP8, PF>;
-  constexpr int kAB = FP8 ? 0 : 1;
+  constexpr int kAB = FP8 || R4 ? 0 : 1;
   constexpr int kTile = L::kTile;
   constexpr uint32_t kIdescPV = idesc_f16(kAB, 1, 128, D);
   Ring rv;
@@ -1127,8 +1128,10 @@ __device__ __forceinline__ bool epi_partial(const Bars& B, uint32_t T, int qt, f
 // and zeroes V rows past the sequence.  fp8 cache: P is f16 (the MMA runs on
 // f16), the converter warps own the raw stages and the zeroing, S is read in
 // two 64-column passes (fewer live registers in the larger block), and the
-// output carries v_scale.
-template <int D, bool FP8, bool PF>
+// output carries v_scale.  R4 (copies of a 4-bit cache's rows): as bf16, but P and V
+// are f16, P = 2^(logit - max + kPExp): three more bits of P, and, as the max is at most
+// 2^8 above the running one, at most 2^14, with the subnormals 2^20 below 1.
+template <int D, bool FP8, bool PF, bool R4>
 __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* smem, const Bars& B,
                              volatile int* abort_flag, uint32_t tmem, Ring& rk, Ring& rv, uint32_t& pt, float sl2,
                              float vscale, PendingEpi& pend, int qt_, int n_ring, bool zero_owner) {
@@ -1242,7 +1245,8 @@ __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* sm
 
     // probabilities two at a time: one packed FMA for the scaled logits, one
     // packed add into the row sum
-    const uint64_t sl2x2 = f32x2(sl2, sl2), nmu2 = f32x2(-mu, -mu);
+    const float nmu = R4 ? kPExp - mu : -mu;
+    const uint64_t sl2x2 = f32x2(sl2, sl2), nmu2 = f32x2(nmu, nmu);
     uint64_t sum2[2] = {0ull, 0ull};
     if constexpr (kRolled) {
       // P of columns 32h .. 32h+31 goes to packed columns 16h .. 16h+15, whose
@@ -1290,7 +1294,7 @@ __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* sm
         f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2x2, nmu2), y0, y1);
         const float p0 = ex2(y0), p1 = ex2(y1);
         sum2[c & 1] = add_f32x2(sum2[c & 1], f32x2(p0, p1));
-        pk[c] = FP8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+        pk[c] = FP8 || R4 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
       }
 #pragma unroll
       for (int c = 0; c < kPass / 64; ++c)
@@ -1368,7 +1372,8 @@ __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* sm
   float* lse_dst = !valid ? nullptr
                    : part ? p.partial_lse + (int64_t)w.partial * kDecodeRows + pr
                           : (p.lse != nullptr ? p.lse + (int64_t)head * p.total_q + tok : nullptr);
-  const float lse = l > 0.f ? (part ? m + __log2f(l) : (m + __log2f(l)) * kLn2) : -INFINITY;
+  const float lse2 = (R4 ? m - kPExp : m) + __log2f(l);
+  const float lse = l > 0.f ? (part ? lse2 : lse2 * kLn2) : -INFINITY;
   if (n > 0 && part) {
     // a split-KV chunk: its partial rows at once (the previous item's deferred
     // epilogue ran in this item's first tile)
@@ -1952,7 +1957,7 @@ __device__ __noinline__ void pass_merges(const AttnParams& p, uint8_t* smem, int
   }
 }
 
-template <int D, bool FP8, bool PF, bool QF8, bool DEC>
+template <int D, bool FP8, bool PF, bool QF8, bool DEC, bool R4>
 __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, volatile int* abort_flag, uint32_t tmem,
                          int it0, int it1) {
   using L = Layout<D, FP8, PF>;
@@ -1966,11 +1971,8 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
         record_status(p.status, PKV_ERR_PLAN_MISMATCH, b, lc);
     }
   }
-  // (bf16: the scales of a 4-bit cache whose rows these are, in the instance that such plans
-  // use; reading them in all of them made the mixed batch's 2% slower)
-  constexpr bool kRows4 = !FP8 && PF && !DEC;
-  const float kscale = FP8 || (kRows4 && p.k_scale != nullptr) ? __ldg(p.k_scale) : 1.f;
-  const float vscale = FP8 || (kRows4 && p.v_scale != nullptr) ? __ldg(p.v_scale) : 1.f;
+  const float kscale = FP8 || R4 ? __ldg(p.k_scale) : 1.f;
+  const float vscale = FP8 || R4 ? __ldg(p.v_scale) : 1.f;
   const float sl2 = p.scale_log2 * kscale;
   // quantised queries: S = codes(Q) . codes(K), times q_scale and k_scale
   const float sl2q = (FP8 && p.q_scale) ? sl2 * __ldg(p.q_scale) : sl2;
@@ -2021,8 +2023,8 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
       const int qt = L::kQQ ? ((threadIdx.x >> 5) - L::kCons0) >> 2 : 0;
       const WorkItem wq = L::kQQ ? q_tile(w, qt, p.causal) : w;
       const bool zero_owner = !L::kQQ || qt == 1 || num_tiles<L::kTile>(q_tile(w, 1, p.causal)) == 0;
-      ok = softmax_item<D, FP8, PF>(p, wq, smem, B, abort_flag, tmem, rk, rv, pt, QF8 ? sl2q : sl2, vscale, pend, qt,
-                                    num_tiles<L::kTile>(w), zero_owner);
+      ok = softmax_item<D, FP8, PF, R4>(p, wq, smem, B, abort_flag, tmem, rk, rv, pt, QF8 ? sl2q : sl2, vscale, pend,
+                                        qt, num_tiles<L::kTile>(w), zero_owner);
     } else {
       ok = false;  // a decode-only launch never receives prefill tiles
     }
@@ -2056,7 +2058,10 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
 // instance without the decode tile's code, whose register demand would
 // otherwise weigh on the softmax path (measured: 133 -> 123 us on the
 // cached-prefix prefill batch).
-template <int D, bool FP8, bool PF, bool QF8, bool DEC>
+// R4: the cache is copies of a 4-bit cache's rows without its tensor scales (K as
+// bf16, V as f16, both exact), in an instance of their own: it holds P in f16, as the
+// other tiles over such a cache do, and reads the scales.
+template <int D, bool FP8, bool PF, bool QF8, bool DEC, bool R4>
 __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, PF>::kCtasPerSm)
     attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q) {
@@ -2171,7 +2176,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
           ok = pv ? pv_issuer_qq<D, FP8, PF>(p, smem, B, abort_flag, tmem, it0, it1)
                   : s_issuer_qq<D, FP8, PF, QF8, DEC>(p, smem, B, abort_flag, tmem, it0, it1);
         else
-          ok = pv ? pv_issuer<D, FP8, PF>(p, smem, B, abort_flag, tmem, it0, it1)
+          ok = pv ? pv_issuer<D, FP8, PF, R4>(p, smem, B, abort_flag, tmem, it0, it1)
                   : s_issuer<D, FP8, PF, QF8, DEC>(p, smem, B, abort_flag, tmem, it0, it1);
         if (!ok) {
           record_status(p.status, PKV_ERR_DEVICE_TIMEOUT, blockIdx.x, pv ? -3 : -1);
@@ -2194,7 +2199,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
       return;
     } else {
       reg_alloc<L::kRegsSoftmax>();
-      consumer<D, FP8, PF, QF8, DEC>(p, smem, B, abort_flag, tmem, it0, it1);
+      consumer<D, FP8, PF, QF8, DEC, R4>(p, smem, B, abort_flag, tmem, it0, it1);
     }
     // the S issuer, the consumers and the P V warp: every tensor-memory access
     // is done before the S issuer's warp frees it
@@ -2225,7 +2230,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
     if constexpr (L::kTc) {
       if (lane == 0) {
         const bool pv = warp == L::kPvWarp;
-        if (!(pv ? pv_issuer<D, FP8, PF>(p, smem, B, abort_flag, tmem, it0, it1)
+        if (!(pv ? pv_issuer<D, FP8, PF, R4>(p, smem, B, abort_flag, tmem, it0, it1)
                  : s_issuer<D, FP8, PF, QF8, DEC>(p, smem, B, abort_flag, tmem, it0, it1))) {
           record_status(p.status, PKV_ERR_DEVICE_TIMEOUT, blockIdx.x, pv ? -3 : -1);
           *abort_flag = 1;
@@ -2238,7 +2243,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
       __syncwarp();
     }
   } else {
-    consumer<D, FP8, PF, QF8, DEC>(p, smem, B, abort_flag, tmem, it0, it1);
+    consumer<D, FP8, PF, QF8, DEC, R4>(p, smem, B, abort_flag, tmem, it0, it1);
   }
   if constexpr (L::kTc) {
     // the S issuer, the consumers and the P V warp: every tensor-memory access
@@ -2250,7 +2255,7 @@ __global__ void __launch_bounds__(Layout<D, FP8, PF>::kThreads, Layout<D, FP8, P
   }
 }
 
-template <int D, bool FP8, bool PF, bool QF8, bool DEC>
+template <int D, bool FP8, bool PF, bool QF8, bool DEC, bool R4 = false>
 cudaError_t launch_t(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                      int num_ctas, bool overlap_prev, cudaStream_t s) {
   using L = Layout<D, FP8, PF>;
@@ -2264,7 +2269,7 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& tk, const CUtensorM
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(attn_kernel<D, FP8, PF, QF8, DEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_kernel<D, FP8, PF, QF8, DEC, R4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              L::kAlloc);
     if (e != cudaSuccess) return e;
     if constexpr (L::kSplitRegs) {
@@ -2272,7 +2277,7 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& tk, const CUtensorM
       // launch: a build with any other count could leave a warpgroup's increase
       // waiting, so it is refused before it runs
       cudaFuncAttributes fa{};
-      e = cudaFuncGetAttributes(&fa, attn_kernel<D, FP8, PF, QF8, DEC>);
+      e = cudaFuncGetAttributes(&fa, attn_kernel<D, FP8, PF, QF8, DEC, R4>);
       if (e != cudaSuccess) return e;
       if (fa.numRegs != L::kLaunchRegs) return cudaErrorInvalidConfiguration;
     }
@@ -2288,7 +2293,7 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& tk, const CUtensorM
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = overlap_prev ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_kernel<D, FP8, PF, QF8, DEC>, p, tk, tv, tq);
+  return cudaLaunchKernelEx(&cfg, attn_kernel<D, FP8, PF, QF8, DEC, R4>, p, tk, tv, tq);
 }
 
 // The instance for a plan: decode-only, prefill-only or mixed; quantised
@@ -2297,6 +2302,12 @@ template <int D, bool FP8, bool QF8>
 cudaError_t launch_kind(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                         int num_ctas, bool has_prefill, bool has_decode, bool o, cudaStream_t s) {
   if (!has_prefill) return launch_t<D, FP8, false, QF8, true>(p, tk, tv, tq, num_ctas, o, s);
+  if constexpr (!FP8) {
+    // (scales over a bf16 cache: copies of a 4-bit cache's rows, whose plans have tensor-core tiles alone)
+    if (p.k_scale)
+      return has_decode ? cudaErrorInvalidValue
+                        : launch_t<D, false, true, false, false, true>(p, tk, tv, tq, num_ctas, o, s);
+  }
   if (!has_decode) return launch_t<D, FP8, true, QF8, false>(p, tk, tv, tq, num_ctas, o, s);
   return launch_t<D, FP8, true, QF8, true>(p, tk, tv, tq, num_ctas, o, s);
 }

@@ -198,9 +198,10 @@ __global__ void __launch_bounds__(kRowThreads) fp4_append_kernel(const AppendPar
 }
 
 // ------------------------------------------------------------------ gather
-// A block of 16 dims, key or value: 32, 16 or 8 + 1 bytes in, 32 out.
+// A block of 16 dims, key or value: 32, 16 or 8 + 1 bytes in, 32 out (f16: code x block scale
+// as f16, without the tensor's scale).
 template <int DT>
-__device__ __forceinline__ void read16(const void* cache, const uint8_t* sf, float scale, uint32_t* w) {
+__device__ __forceinline__ void read16(const void* cache, const uint8_t* sf, float scale, bool f16, uint32_t* w) {
   uint32_t h[8];
   if constexpr (DT == PKV_FP8_E4M3) {
     const uint4 c = __ldg(static_cast<const uint4*>(cache));
@@ -216,6 +217,11 @@ __device__ __forceinline__ void read16(const void* cache, const uint8_t* sf, flo
     // (code * block scale has six significant bits: exact)
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = mul_f16x2(h[i], s);
+  }
+  if (f16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = h[i];
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherParams 
       if constexpr (DT == PKV_BF16)
         load16(reinterpret_cast<const __nv_bfloat16*>(cache + k * half * kBytes), wide & 1, w[x][k]);
       else
-        read16<DT>(cache + k * half * kBytes, sf + k * half, f, w[x][k]);
+        read16<DT>(cache + k * half * kBytes, sf + k * half, f, x == 1 && p.lens != nullptr, w[x][k]);
     }
   }
 #pragma unroll

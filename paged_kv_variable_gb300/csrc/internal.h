@@ -132,7 +132,7 @@ struct FarLayout {
   size_t indptr;    // int32[B + 1] its pages
   size_t table;     // int32[pages] page numbers
   size_t lens;      // int32[B] its keys
-  size_t k, v;      // the copies: (pages, kFarPage, Hkv, D) bf16
+  size_t k, v;      // the copies: (pages, kFarPage, Hkv, D) bf16 and f16
   int32_t pages;
 };
 constexpr int kFarPage = 128;
@@ -163,7 +163,7 @@ struct pkv_plan_s {
   int32_t shared;   // some prefix is computed once for several sequences
   // 4-bit cache
   int32_t max_rows;     // rows of the largest tile
-  pkv_plan_s* far;      // nullable: the sequences whose queries fill tensor-core tiles, over bf16 copies of
+  pkv_plan_s* far;      // nullable: the sequences whose queries fill tensor-core tiles, over 16-bit copies of
                         // their keys and values in the workspace
   pkv::FarLayout far_layout;
   int32_t row_combine;  // made by pkv_plan_shared_prefix: merged a warp (or block) a row

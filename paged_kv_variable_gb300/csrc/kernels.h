@@ -77,8 +77,8 @@ struct GatherParams {
   Fp4Scales sf;
   const float* k_scale;  // nullable: 1
   const float* v_scale;
-  const int32_t* lens;   // nullable (copies that an attention reads, k_out and v_out given): [batch] rows of a
-                         // sequence past these are left out, those of a page out of range zeros
+  const int32_t* lens;   // nullable (copies that an attention reads: k_out bf16, v_out f16, both given): [batch]
+                         // rows of a sequence past these are left out, those of a page out of range zeros
   const int32_t* cache_seqlens;  // (with lens) compared with the lengths of the plan
   const int32_t* plan_lc;
   int* status;
@@ -118,7 +118,7 @@ struct AttnParams {
   int32_t G;
   int32_t causal;
   float scale_log2;    // softmax_scale * log2(e)
-  const float* k_scale;  // (bf16 cache: nullable)
+  const float* k_scale;  // (bf16 cache: null, or the cache is copies of a 4-bit one's rows, K as bf16 and V as f16)
   const float* v_scale;
   const float* q_scale;  // nullable (fp8 cache, decode tiles): Q quantised to e4m3 for Q K^T
   const WorkItem* items;

@@ -291,7 +291,7 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
 // Time model (us, from measurements on a GB300, D = 128; the rest by bytes and
 // flops) of the two ways to attend the keys of a sequence over a 4-bit cache: tiles
 // of 16 rows straight from it, each a pass over the keys, or tensor-core tiles of
-// 128 over bf16 copies of its rows, made first.  On 21 batches of 5 to 2048 queries a
+// 128 over 16-bit copies of its rows, made first.  On 21 batches of 5 to 2048 queries a
 // sequence the choice is the faster one but for one batch (20.1 against 14.9 us).  Without
 // the tiles' starts it took the slower way for 189 sequences of 16 queries and 22 to 45
 // keys (93 against 36 us), without the longest tile's own time for two of 58 queries

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import long_cache as LC
-from tests.test_fp4 import attend
+from tests.test_fp4 import attend, check
 
 
 @pytest.fixture(scope="module")
@@ -68,3 +68,31 @@ def test_rows_that_no_copy_writes_are_not_seen(pkv, page):
     pkv.attn_varlen_kvcache_fwd(prob, args, plan, ws)
     assert pkv.get_status(ws) == 0
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# ------------------------------------------------------------------ precision
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_scale", [1.5, 4.0])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_are_as_precise_as_decode_steps(pkv, d, q_scale, causal):
+    """The bound of the tiles straight over the cache (P rounded to 11 bits, kept above the subnormals) holds for prompts
+    over copies too: with sharp logits few keys take the weight, and the roundings of P do not average out."""
+    lens, lq = [900, 1537, 65], [700, 300, 65]
+    cache = LC.Cache(83, dtype="fp4", lens=lens, hkv=4, d=d, page=16)
+    q, out, lse, plan, ws, args, prob = attend(pkv, cache, 16, lq, [0] * 3, causal=causal, q_scale=q_scale)
+    assert {it["kind"] for it in plan.items()} == {1}
+    check(cache, out, lse, q, lq, lens, causal)
+
+
+@pytest.mark.gpu
+def test_prompts_with_few_keys_of_weight(pkv):
+    """Values of 0 under all keys but those with the smallest weights: a weight far below the largest one counts."""
+    lens, lq, hkv, d = [640], [512], 2, 128
+    x = np.random.default_rng(5).standard_normal((2, 640, hkv, d))
+    x[1, :320] = 0                       # (causal: the first rows see zeros alone)
+    x[0, :320] *= 3
+    cache = LC.Cache(84, dtype="fp4", lens=lens, hkv=hkv, d=d, page=16, values=x)
+    q, out, lse, plan, ws, args, prob = attend(pkv, cache, 32, lq, [0], causal=False, q_scale=4.0)
+    assert {it["kind"] for it in plan.items()} == {1}
+    check(cache, out, lse, q, lq, lens, False)
