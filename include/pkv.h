@@ -191,7 +191,7 @@ typedef struct {
  * CTA each, whatever the query length; sequences whose many query rows make it
  * worth it are attended by the tensor-core tiles over 16-bit copies of their cached
  * rows, which the call makes in the workspace: 4 * head_dim bytes a key and kv
- * head, in all at most 4 GiB (a batch that needs more is planned without).  Their
+ * head, in all at most 4 GiB (sequences beyond are planned without).  Their
  * cache lengths have to be the plan's.  At most 2^30 keys a sequence.
  * h_q_lens / h_cache_lens / h_new_lens: host int32 [B]; h_new_lens may be NULL
  * when the call appends nothing.  Zero lengths are accepted.  On success

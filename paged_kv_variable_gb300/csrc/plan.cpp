@@ -359,25 +359,35 @@ pkv_status make_fp4_plan(const pkv_problem& p, const int32_t* h_q_lens, const in
     const double longest = lq > tq128 ? lk * Fp4Model::kKeyAlone * D / 128.0 : 0.0;
     if (!dynamic && lk > 0 && near > far) choices.push_back({b, near, far, longest});
   }
-  // of those, the sequences up to some length: few long tiles leave SMs idle
-  std::sort(choices.begin(), choices.end(), [](const Choice& x, const Choice& y) { return x.longest < y.longest; });
+  // of those, the sequences up to some length: few long tiles leave SMs idle; and as many of
+  // them as the bytes of the copies allow (one that does not fit stays out, the others do not)
+  std::sort(choices.begin(), choices.end(), [](const Choice& x, const Choice& y) {
+    return x.longest != y.longest ? x.longest < y.longest : x.b < y.b;
+  });
+  auto keys_of = [&](int b) { return h_cache_lens[b] + (h_new_lens ? h_new_lens[b] : 0); };
+  auto pages_of = [&](int b) { return ((int64_t)keys_of(b) + kFarPage - 1) / kFarPage; };
+  const size_t far_row = sizeof(uint16_t) * (size_t)p.num_heads_kv * D;  // a token's keys (or values)
+  const int64_t most_pages = (int64_t)(Fp4Model::kMostCopied / (far_row * 2 * kFarPage));
   double best_gain = Fp4Model::kLaunches, near_sum = 0, far_sum = 0;
+  std::vector<Choice> fit;
   size_t taken = 0;
-  for (size_t i = 0; i < choices.size(); ++i) {
-    near_sum += choices[i].near;
-    far_sum += choices[i].far;
-    const double gain = near_sum - std::max(far_sum, choices[i].longest);
-    if (gain > best_gain) best_gain = gain, taken = i + 1;
+  int64_t pages = 0;
+  for (const Choice& c : choices) {
+    if (pages + pages_of(c.b) > most_pages) continue;
+    pages += pages_of(c.b);
+    fit.push_back(c);
+    near_sum += c.near;
+    far_sum += c.far;
+    const double gain = near_sum - std::max(far_sum, c.longest);
+    if (gain > best_gain) best_gain = gain, taken = fit.size();
   }
   int64_t far_pages = 0;
   for (size_t i = 0; i < taken; ++i) {
-    const int b = choices[i].b;
+    const int b = fit[i].b;
     far_q[b] = h_q_lens[b];
-    far_keys[b] = h_cache_lens[b] + (h_new_lens ? h_new_lens[b] : 0);
-    far_pages += (far_keys[b] + kFarPage - 1) / kFarPage;
+    far_keys[b] = keys_of(b);
+    far_pages += pages_of(b);
   }
-  const size_t far_row = sizeof(uint16_t) * (size_t)p.num_heads_kv * D;  // a token's keys (or values)
-  if ((double)far_pages * kFarPage * far_row * 2 > (double)Fp4Model::kMostCopied) far_pages = 0;
   // the sequences with many queries: a plan of its own over the copies, pages in order
   std::unique_ptr<pkv_plan_s, void (*)(pkv_plan_t)> far(nullptr, pkv_plan_destroy);
   if (far_pages > 0) {

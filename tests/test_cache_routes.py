@@ -96,3 +96,32 @@ def test_prompts_with_few_keys_of_weight(pkv):
     q, out, lse, plan, ws, args, prob = attend(pkv, cache, 32, lq, [0], causal=False, q_scale=4.0)
     assert {it["kind"] for it in plan.items()} == {1}
     check(cache, out, lse, q, lq, lens, False)
+
+
+# ------------------------------------------------------------------ the bytes of the copies
+def kinds_of(pkv, lq, lens, hq, hkv, d):
+    prob = pkv.make_problem(batch=len(lq), num_heads_q=hq, num_heads_kv=hkv, head_dim=d, page_size=64,
+                            cache_capacity=-(-max(lens) // 64) * 64, num_pages=1 << 18, cache_dtype="fp4", causal=True,
+                            softmax_scale=0.1)
+    plan = pkv.plan(prob, lq, lens, None, num_sms=152)
+    kinds = {}
+    for it in plan.items():
+        kinds.setdefault(it["seq"], set()).add(it["kind"])
+    return [kinds[b] for b in range(len(lq))], plan.workspace_bytes
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (32, 8, 64), (16, 4, 256)])
+def test_copies_up_to_their_bound(pkv, hq, hkv, d):
+    """Prompts that fill the 4 GiB of copies keep them when more come; those that do not fit go without."""
+    token = 4 * d * hkv
+    keys = 16384 * 4096 // token
+    full = (4 << 30) // (token * keys)
+    for more in (0, 1, 7):
+        kinds, size = kinds_of(pkv, [512] * (full + more), [keys] * (full + more), hq, hkv, d)
+        assert [k == {1} for k in kinds].count(True) == full and [k == {0} for k in kinds].count(True) == more
+        assert (4 << 30) < size < (4 << 30) + (64 << 20)
+    # a long one that does not fit beside the others does not keep them out, nor a short one behind it
+    kinds, _ = kinds_of(pkv, [512] * (full - 1) + [1024, 512], [keys] * (full - 1) + [2 * keys, keys // 2], hq, hkv, d)
+    assert kinds == [{1}] * (full - 1) + [{0}, {1}]
+    kinds, _ = kinds_of(pkv, [256] * (full // 2) + [64], [2 * keys] * (full // 2) + [2048], hq, hkv, d)
+    assert kinds.count({1}) >= full // 2 and len(kinds) == full // 2 + 1
