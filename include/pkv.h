@@ -331,7 +331,9 @@ pkv_status pkv_attn_varlen_kvcache_fwd(const pkv_problem* problem, const pkv_fwd
  *  - The first call on a device resolves the array's device address
  *    (cudaGetSymbolAddress, checked) with that device current, once.
  *  - A plan needing more than 32 MiB of workspace is rejected with
- *    PKV_ERR_WORKSPACE_TOO_SMALL before anything is launched.
+ *    PKV_ERR_WORKSPACE_TOO_SMALL before anything is launched.  One over an fp4
+ *    cache that has copies of rows goes without them (the first such call of a
+ *    plan makes that work list, in host memory, and the plan keeps it).
  *  - Every host-side check (problem, plan, cache, q / out, new tokens, size)
  *    runs before the array is touched: a rejected call copies nothing.
  *  - Every call on a device shares the one array: calls that overlap on the

@@ -166,6 +166,9 @@ struct pkv_plan_s {
   pkv_plan_s* far;      // nullable: the sequences whose queries fill tensor-core tiles, over 16-bit copies of
                         // their keys and values in the workspace
   pkv::FarLayout far_layout;
+  int32_t* lens;        // (with far) [3][batch] what the plan was made from: lengths of queries, cache, new tokens
+  int32_t num_sms;
+  pkv_plan_s* direct;   // nullable: the same without copies, once a call has needed it
   int32_t row_combine;  // made by pkv_plan_shared_prefix: merged a warp (or block) a row
   double* item_cost;  // [num_items] model cost of each item, in work-list order
 };
@@ -175,4 +178,6 @@ namespace pkv {
 pkv_status fail(pkv_status st, const char* fmt, ...);
 // host checks of an attention call other than its workspace (api.cu)
 pkv_status validate_call(const pkv_problem* problem, const pkv_fwd_args* args, pkv_plan_t plan);
+// the tiles of a 4-bit plan that has copies, straight over the cache (kept with the plan) (plan.cpp)
+pkv_status plan_without_copies(pkv_plan_t plan, pkv_plan_t* out);
 }  // namespace pkv

@@ -17,7 +17,8 @@ namespace pkv {
 namespace {
 
 // The fixed scratch: 32 MiB per device.  A plan whose workspace is larger is
-// rejected (split-KV partials dominate: 8 KiB per KV chunk at head_dim 128).
+// rejected (split-KV partials dominate: 8 KiB per KV chunk at head_dim 128), but
+// that a 4-bit cache's prompts go without the copies of their rows.
 constexpr size_t kStaticScratchBytes = size_t(32) << 20;
 static __device__ __align__(256) unsigned char g_static_scratch[kStaticScratchBytes];
 
@@ -53,6 +54,11 @@ extern "C" pkv_status pkv_attn_varlen_kvcache_fwd_noalloc(const pkv_problem* pro
   // every host check first: a rejected call leaves the shared scratch alone
   pkv_status st = validate_call(problem, args, plan);
   if (st != PKV_OK) return st;
+  if (plan->layout.total > kStaticScratchBytes && plan->far) {
+    // copies of a 4-bit cache's rows that do not fit: every tile straight over the cache
+    st = plan_without_copies(plan, &plan);
+    if (st != PKV_OK) return st;
+  }
   if (plan->layout.total > kStaticScratchBytes)
     return fail(PKV_ERR_WORKSPACE_TOO_SMALL,
                 "this plan needs %zu bytes of scratch but the fixed scratch holds %zu bytes; use "

@@ -17,6 +17,7 @@
 #include <exception>
 #include <functional>
 #include <memory>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -317,8 +318,8 @@ struct Fp4Model {
 // chunk of them.  A block of its own runs each tile, longest first: the hardware
 // hands the next one to whichever SM has room (four blocks an SM).
 pkv_status make_fp4_plan(const pkv_problem& p, const int32_t* h_q_lens, const int32_t* h_cache_lens,
-                         const int32_t* h_new_lens, int32_t num_sms, bool dynamic, pkv_plan_t* out_plan,
-                         size_t* out_workspace_bytes) {
+                         const int32_t* h_new_lens, int32_t num_sms, bool dynamic, size_t most_copied,
+                         pkv_plan_t* out_plan, size_t* out_workspace_bytes) {
   const int B = p.batch, G = p.num_heads_q / p.num_heads_kv, D = p.head_dim;
   const int cap = fp4_rows(D);
   const int nh_tile = std::min(G, cap), tq = cap / nh_tile;
@@ -367,7 +368,7 @@ pkv_status make_fp4_plan(const pkv_problem& p, const int32_t* h_q_lens, const in
   auto keys_of = [&](int b) { return h_cache_lens[b] + (h_new_lens ? h_new_lens[b] : 0); };
   auto pages_of = [&](int b) { return ((int64_t)keys_of(b) + kFarPage - 1) / kFarPage; };
   const size_t far_row = sizeof(uint16_t) * (size_t)p.num_heads_kv * D;  // a token's keys (or values)
-  const int64_t most_pages = (int64_t)(Fp4Model::kMostCopied / (far_row * 2 * kFarPage));
+  const int64_t most_pages = (int64_t)(most_copied / (far_row * 2 * kFarPage));
   double best_gain = Fp4Model::kLaunches, near_sum = 0, far_sum = 0;
   std::vector<Choice> fit;
   size_t taken = 0;
@@ -561,13 +562,13 @@ pkv_status make_fp4_plan(const pkv_problem& p, const int32_t* h_q_lens, const in
   if (!plan) return fail(PKV_ERR_INVALID_ARG, "out of host memory");
   plan->image = (unsigned char*)calloc(1, image_bytes);
   plan->item_cost = (double*)calloc((size_t)std::max(1, num_items), sizeof(double));
-  if (!plan->image || !plan->item_cost) {
-    free(plan->image);
-    free(plan->item_cost);
-    delete plan;
+  if (far) plan->lens = (int32_t*)calloc((size_t)3 * B, sizeof(int32_t));
+  if (!plan->image || !plan->item_cost || (far && !plan->lens)) {
+    pkv_plan_destroy(plan);
     return fail(PKV_ERR_INVALID_ARG, "out of host memory");
   }
   plan->problem = p;
+  plan->num_sms = num_sms;
   plan->num_ctas = num_items;
   plan->num_slots = (int32_t)num_slots;
   plan->total_q = (int32_t)total_q;
@@ -606,6 +607,9 @@ pkv_status make_fp4_plan(const pkv_problem& p, const int32_t* h_q_lens, const in
       ints(F.lens)[b] = far_keys[b];
     }
     for (int i = 0; i < F.pages; ++i) ints(F.table)[i] = i;
+    std::copy_n(h_q_lens, B, plan->lens);
+    std::copy_n(h_cache_lens, B, plan->lens + B);
+    if (h_new_lens) std::copy_n(h_new_lens, B, plan->lens + 2 * B);
     memcpy(plan->image + F.plan, far->image, far->image_bytes);
     plan->num_prefill_items = far->num_prefill_items;
     plan->num_split_units += far->num_split_units;
@@ -631,7 +635,8 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
   if (num_sms <= 0) return fail(PKV_ERR_INVALID_ARG, "num_sms must be positive");
   if (p.cache_dtype == PKV_FP4_E2M1) {
     if (groups != nullptr) return fail(PKV_ERR_UNSUPPORTED, "shared prefixes take bf16 and fp8 caches");
-    return make_fp4_plan(p, h_q_lens, h_cache_lens, h_new_lens, num_sms, dynamic, out_plan, out_workspace_bytes);
+    return make_fp4_plan(p, h_q_lens, h_cache_lens, h_new_lens, num_sms, dynamic, Fp4Model::kMostCopied, out_plan,
+                         out_workspace_bytes);
   }
 
   const int G = p.num_heads_q / p.num_heads_kv;
@@ -1136,17 +1141,41 @@ pkv_status make_plan(const pkv_problem* problem, const int32_t* h_q_lens, const 
 
 namespace {
 
-// make_plan for the C entries: what the containers throw becomes a status.
-template <class... Args>
-pkv_status make_plan_noexcept(Args... args) noexcept {
+// For the C entries: what the containers throw becomes a status.
+template <class F>
+pkv_status no_exceptions(F&& f) noexcept {
   try {
-    return make_plan(args...);
+    return f();
   } catch (const std::exception&) {
     return fail(PKV_ERR_INVALID_ARG, "out of host memory");
   }
 }
+template <class... Args>
+pkv_status make_plan_noexcept(Args... args) noexcept {
+  return no_exceptions([&] { return make_plan(args...); });
+}
 
 }  // namespace
+
+namespace pkv {
+
+pkv_status plan_without_copies(pkv_plan_t plan, pkv_plan_t* out) {
+  static std::mutex mu;
+  return no_exceptions([&] {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!plan->direct) {
+      const int B = plan->problem.batch;
+      size_t bytes = 0;
+      const pkv_status st = make_fp4_plan(plan->problem, plan->lens, plan->lens + B, plan->lens + 2 * B, plan->num_sms,
+                                          false, 0, &plan->direct, &bytes);
+      if (st != PKV_OK) return st;
+    }
+    *out = plan->direct;
+    return PKV_OK;
+  });
+}
+
+}  // namespace pkv
 
 extern "C" pkv_status pkv_plan(const pkv_problem* problem, const int32_t* h_q_lens,
                                const int32_t* h_cache_lens, const int32_t* h_new_lens,
@@ -1229,6 +1258,8 @@ extern "C" pkv_status pkv_plan_get_items(pkv_plan_t plan, pkv_work_item* h_items
 extern "C" void pkv_plan_destroy(pkv_plan_t plan) {
   if (!plan) return;
   pkv_plan_destroy(plan->far);
+  pkv_plan_destroy(plan->direct);
+  free(plan->lens);
   free(plan->image);
   free(plan->item_cost);
   delete plan;

@@ -125,3 +125,22 @@ def test_copies_up_to_their_bound(pkv, hq, hkv, d):
     assert kinds == [{1}] * (full - 1) + [{0}, {1}]
     kinds, _ = kinds_of(pkv, [256] * (full // 2) + [64], [2 * keys] * (full // 2) + [2048], hq, hkv, d)
     assert kinds.count({1}) >= full // 2 and len(kinds) == full // 2 + 1
+
+
+@pytest.mark.gpu
+def test_prompts_without_a_workspace(pkv):
+    """A prompt whose copies would not fit the fixed scratch is attended straight over the cache; what was planned stays."""
+    lens, lq, hq = [8200, 40], [300, 1], 16
+    cache = LC.Cache(88, dtype="fp4", lens=lens, hkv=8, d=128, page=16)
+    q, out, lse, plan, ws, args, prob = attend(pkv, cache, hq, lq, [3, 1])
+    assert {(it["seq"], it["kind"]) for it in plan.items()} == {(0, 1), (1, 0)} and plan.workspace_bytes > 32 << 20
+    for _ in range(2):
+        out.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        pkv.attn_varlen_kvcache_fwd_noalloc(prob, args, plan)
+        assert pkv.get_status_noalloc() == 0
+        check(cache, out, lse, q, lq, lens, True)
+    assert {(it["seq"], it["kind"]) for it in plan.items()} == {(0, 1), (1, 0)}
+    args.keep[5][0] -= 1  # lengths other than the plan's
+    pkv.attn_varlen_kvcache_fwd_noalloc(prob, args, plan)
+    assert pkv.get_status_noalloc() == 7
