@@ -230,8 +230,9 @@ __global__ void __launch_bounds__(kThreads, fp4_blocks(D, 8 * NQ))
   }
 
   // ------------------------------------------------------------------ queries
-  // Q^T (B operand): row 8j + g, dims as K's lanes have them
+  // Q^T (B operand): row 8j + g, dims as K's lanes have them, in f16
   uint32_t qb[NQ][KS][2];
+  bool odd = false;  // some number is not an f16 number (of eight bits: 0, or from 2^-17 below 2^16)
 #pragma unroll
   for (int j = 0; j < NQ; ++j) {
     const int r = 8 * j + g;
@@ -242,12 +243,36 @@ __global__ void __launch_bounds__(kThreads, fp4_blocks(D, 8 * NQ))
     for (int c = 0; c < D / 32; ++c) {  // eight dims at a time
       const int d0 = D == 64 ? 16 * t + 8 * c : 32 * t + 8 * (c & 3) + 128 * (c >> 2);
       const uint4 v = qr ? __ldg(reinterpret_cast<const uint4*>(qr + d0)) : make_uint4(0, 0, 0, 0);
-      qb[j][2 * c][0] = bf16x2_to_f16x2(v.x);
-      qb[j][2 * c][1] = bf16x2_to_f16x2(v.y);
-      qb[j][2 * c + 1][0] = bf16x2_to_f16x2(v.z);
-      qb[j][2 * c + 1][1] = bf16x2_to_f16x2(v.w);
+      qb[j][2 * c][0] = v.x, qb[j][2 * c][1] = v.y, qb[j][2 * c + 1][0] = v.z, qb[j][2 * c + 1][1] = v.w;
     }
+    odd |= !f16_numbers(qb[j][0], 2 * KS);
   }
+  // Then each row is taken times a power of two, which its logits take out again.  (In every tile
+  // that took 1% more time on long sequences, 4 to 8% with tiles of 16 and 32 rows; of tiles of
+  // normally distributed queries less than one in a hundred needs it.)
+  __shared__ __align__(8) float downs[kWarps][8 * NQ];
+  const bool scaled = __any_sync(0xffffffffu, odd);
+  if (scaled) {
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) most = bf16x2_most(qb[j][k][1], bf16x2_most(qb[j][k][0], most));
+      const RowScale scale(most_of_row(most));
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qb[j][k][e] = scale.times(qb[j][k][e]);
+      if (t == 0) downs[warp][8 * j + g] = scale.down();
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qb[j][k][e] = bf16x2_to_f16x2(qb[j][k][e]);
   // keys that this lane's query rows (columns 2t, 2t + 1 of S^T) see
   int lim[NQ][2];
 #pragma unroll
@@ -339,6 +364,15 @@ __global__ void __launch_bounds__(kThreads, fp4_blocks(D, 8 * NQ))
           mma_f16(s[j][x], a[0], b[0], a[1], b[1], qb[j][2 * c][0], qb[j][2 * c][1]);
           mma_f16(s[j][x], a[2], b[2], a[3], b[3], qb[j][2 * c + 1][0], qb[j][2 * c + 1][1]);
         }
+      }
+    }
+
+    if (scaled) {
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        const float2 d = *reinterpret_cast<const float2*>(&downs[warp][8 * j + 2 * t]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) s[j][x][0] *= d.x, s[j][x][1] *= d.y, s[j][x][2] *= d.x, s[j][x][3] *= d.y;
       }
     }
 

@@ -98,6 +98,61 @@ def test_prompts_with_few_keys_of_weight(pkv):
     check(cache, out, lse, q, lq, lens, False)
 
 
+# ------------------------------------------------------------------ the range of the queries
+def scaled(pkv, cache, q, lq, power, hq, causal=True, softmax_scale=None, routes=None):
+    """Outputs for q 2^power and the softmax's scale 2^-power: the same numbers, but for what a narrower type loses."""
+    rows = sum(lq)
+    out = torch.full((rows, hq, cache.d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((hq, rows), float("nan"), dtype=torch.float32, device="cuda")
+    prob = cache.problem(pkv, hq, causal, (softmax_scale or cache.d ** -0.5) * 2.0 ** -power)
+    plan = pkv.plan(prob, lq, cache.lens)
+    ws = pkv.workspace_tensor(plan.workspace_bytes)
+    plan.upload(ws)
+    q = (q.double() * 2.0 ** power).bfloat16()
+    args = cache.args(pkv, q=q, out=out, lse=lse, cu_seqlens_q=LC.i32(np.cumsum([0] + lq)), max_seqlen_q=max(lq))
+    pkv.attn_varlen_kvcache_fwd(prob, args, plan, ws)
+    assert pkv.get_status(ws) == 0
+    if routes is not None:
+        assert {it["kind"] for it in plan.items()} == routes
+    return out, lse, args, prob
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq,hkv", [(64, 32, 4), (64, 32, 1), (128, 16, 4), (256, 8, 2)])
+@pytest.mark.parametrize("power", [-100, -20, 20, 100])
+def test_queries_of_any_magnitude(pkv, d, hq, hkv, power):
+    """Queries near both ends of bf16's range, decode steps, drafts and prompts: the bits of the ordinary ones."""
+    lens, lq = [700, 300, 129, 33, 900], [1, 1, 3, 1, 700]
+    cache = LC.Cache(85, dtype="fp4", lens=lens, hkv=hkv, d=d, page=16)
+    g = torch.Generator().manual_seed(6)
+    q = (1.5 * torch.randn(sum(lq), hq, d, generator=g)).bfloat16().cuda()
+    want = scaled(pkv, cache, q, lq, 0, hq, routes={0, 1})
+    check(cache, want[0], want[1], q, lq, lens, True)
+    got = scaled(pkv, cache, q, lq, power, hq)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq", [(64, 16), (64, 32), (128, 16), (256, 8)])
+def test_rows_of_different_magnitudes_in_one_tile(pkv, d, hq):
+    """Heads of a group from 2^-40 to 2^40 of one another, one of zeros, one with an infinity, which shows in no other."""
+    lens, lq = [300, 40], [1, 1]
+    cache = LC.Cache(86, dtype="fp4", lens=lens, hkv=1, d=d, page=16)
+    g = torch.Generator().manual_seed(7)
+    q = torch.randn(2, hq, d, generator=g).double().cuda()
+    q = (q * torch.tensor([2.0 ** (20 * (h % 5 - 2)) for h in range(hq)], device="cuda").double()[None, :, None]).bfloat16()
+    q[:, 3] = 0
+    clean, q[:, 5, 7] = q.clone(), float("inf")
+    want = scaled(pkv, cache, clean, lq, 0, hq)
+    got = scaled(pkv, cache, q, lq, 0, hq)
+    others = [h for h in range(hq) if h != 5]
+    assert torch.equal(got[0][:, others], want[0][:, others]) and torch.equal(got[1][others], want[1][others])
+    for h in range(hq):  # each head's row alone
+        one = scaled(pkv, cache, clean[:, h:h + 1].contiguous(), lq, 0, 1)
+        check(cache, one[0], one[1], clean[:, h:h + 1], lq, lens, True)
+    check(cache, want[0], want[1], clean, lq, lens, True)
+
+
 # ------------------------------------------------------------------ the bytes of the copies
 def kinds_of(pkv, lq, lens, hq, hkv, d):
     prob = pkv.make_problem(batch=len(lq), num_heads_q=hq, num_heads_kv=hkv, head_dim=d, page_size=64,
