@@ -37,8 +37,8 @@
  *    their own (k_sf, v_sf): value = code * block scale * tensor scale (k_scale,
  *    v_scale).  A row takes D/2 + D/16 bytes.  Its cache strides are in BYTES.
  *  - Queries meet the keys of an fp8 cache as f16: exact from 2^-17 below 65536 in
- *    magnitude.  Over an fp4 cache a row beyond is scaled by a power of two on the
- *    way; only its dims 2^-31 and more below its largest lose bits.
+ *    magnitude.  Over an fp4 cache, and in pkv_attn_weights, a row beyond is scaled by
+ *    a power of two on the way; only its dims 2^-31 and more below its largest lose bits.
  *  - Strides are in ELEMENTS (of the tensor's own type).  The innermost
  *    (head_dim) stride is 1.  All base pointers must be 16-byte aligned and all
  *    strides multiples of 16 bytes.

@@ -15,7 +15,7 @@
 // Many rows (a window of queries, a prompt): the keys of a step stay in registers and
 // the queries pass by from shared memory, where the block puts them in the order of
 // the MMA's operand (128 rows at a time).  The warp MMAs and exponentials bound it: 32
-// queries a sequence of 8 prompts of 5000 to 16384 fp8 keys, 128 rows a kv head, 77.3 us, of
+// queries a sequence of 8 prompts of 5000 to 16384 fp8 keys, 128 rows a kv head, 76.0 us, of
 // which the MMAs at their rate would take 37.  (The same with S^T = K Q^T by tcgen05 MMAs, a key
 // a thread, the queries staged as operands (an fp8 one as two e4m3 terms): 88 us, for the
 // staging took 5 us of each block and two blocks filled an SM.)
@@ -92,13 +92,17 @@ struct Row {
   }
 };
 
-// Eight dims of a query row as operand registers (zeros where qr is null).
-template <int DT>
+// Eight dims of a query row (zeros where qr is null).  Over a cache that is not bf16 they
+// become f16, times a power of two of the row's (RowScale), which its logits take out again.
 __device__ __forceinline__ uint4 query8(const __nv_bfloat16* qr, int d0) {
-  uint4 v = qr ? __ldg(reinterpret_cast<const uint4*>(qr + d0)) : make_uint4(0, 0, 0, 0);
-  if constexpr (DT != PKV_BF16)
-    v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
-  return v;
+  return qr ? __ldg(reinterpret_cast<const uint4*>(qr + d0)) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t most8(const uint4& v, uint32_t most) {
+  return bf16x2_most(v.x, bf16x2_most(v.y, bf16x2_most(v.z, bf16x2_most(v.w, most))));
+}
+__device__ __forceinline__ uint4 f16x8(const uint4& v, const RowScale& s) {
+  return make_uint4(bf16x2_to_f16x2(s.times(v.x)), bf16x2_to_f16x2(s.times(v.y)), bf16x2_to_f16x2(s.times(v.z)),
+                    bf16x2_to_f16x2(s.times(v.w)));
 }
 
 template <int DT>
@@ -325,21 +329,33 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NQ == 2 ? 2 : 3)
   Sums<S::kKeys> sums(p, b, hk);
   sums.load(keys, 0);
 
+  const float sl2 = p.scale_log2 * (p.k_scale != nullptr ? __ldg(p.k_scale) : 1.f);
   uint32_t qw[NQ][W];
-  float l2[NQ][2];
+  float l2[NQ][2], sl2r[NQ][2];
   int lim[NQ][2];
 #pragma unroll
   for (int j = 0; j < NQ; ++j) {
     const __nv_bfloat16* qr = query_row(p, s, hk, 8 * j + g);
+    uint4 v[W / 4];
 #pragma unroll
-    for (int c = 0; c < W / 4; ++c) {
-      const uint4 v = query8<DT>(qr, R::dim(c, t));
-      qw[j][4 * c] = v.x, qw[j][4 * c + 1] = v.y, qw[j][4 * c + 2] = v.z, qw[j][4 * c + 3] = v.w;
+    for (int c = 0; c < W / 4; ++c) v[c] = query8(qr, R::dim(c, t));
+    sl2r[j][0] = sl2r[j][1] = sl2;
+    if constexpr (DT != PKV_BF16) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int c = 0; c < W / 4; ++c) most = most8(v[c], most);
+      const RowScale scale(most_of_row(most));
+#pragma unroll
+      for (int c = 0; c < W / 4; ++c) v[c] = f16x8(v[c], scale);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sl2r[j][e] *= __shfl_sync(0xffffffffu, scale.down(), 4 * (2 * t + e));
     }
+#pragma unroll
+    for (int c = 0; c < W / 4; ++c)
+      qw[j][4 * c] = v[c].x, qw[j][4 * c + 1] = v[c].y, qw[j][4 * c + 2] = v[c].z, qw[j][4 * c + 3] = v[c].w;
     row_info(p, s, hk, 8 * j + 2 * t, l2[j][0], lim[j][0]);
     row_info(p, s, hk, 8 * j + 2 * t + 1, l2[j][1], lim[j][1]);
   }
-  const float sl2 = p.scale_log2 * (p.k_scale != nullptr ? __ldg(p.k_scale) : 1.f);
 
   for (int i = 0; i < keys.mine; ++i) {
     keys.next(i);
@@ -362,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NQ == 2 ? 2 : 3)
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float w = ex2(fmaf(c[2 * h + e], sl2, -l2[j][e]));
+            const float w = ex2(fmaf(c[2 * h + e], sl2r[j][e], -l2[j][e]));
             sum[x][h] += t0 + 16 * x + 8 * h + g < lim[j][e] ? w : 0.f;
           }
       }
@@ -389,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
   using L = Many<D, DT>;
   constexpr int MT = S::kKeys / 16, W = R::kWords;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) float s_l2[L::kRows];
+  // of two rows each: their log2-domain LSEs, and the scales of their logits
+  __shared__ __align__(16) float4 s_row[L::kRows / 2];
   __shared__ __align__(8) int s_lim[L::kRows];
   uint4* qs = reinterpret_cast<uint4*>(smem);  // [tile of 8 rows][W / 4][lane]
   const int b = blockIdx.z, hk = blockIdx.y;
@@ -402,21 +419,39 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
   sums.load(keys, 0);
   const float sl2 = p.scale_log2 * (p.k_scale != nullptr ? __ldg(p.k_scale) : 1.f);
 
-  // rows r0 .. r0 + n - 1 into shared memory, in the order of the operand; every load of a
-  // thread's in flight at once
+  // rows r0 .. r0 + n - 1 into shared memory, in the order of the operand, a warp eight rows at a
+  // time; every load of a thread's in flight at once
   auto stage = [&](int r0, int n) {
-    constexpr int kEach = L::kRows / 8 * (W / 4) * 32 / kThreads;
-    const int all = (n + 7) / 8 * (W / 4) * 32;
-    uint4 v[kEach];
+    constexpr int kEach = L::kRows / 8 / kWarps;  // tiles of eight rows a warp
+    const int tile0 = threadIdx.x >> 5;
+    uint4 v[kEach][W / 4];
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int i = threadIdx.x + k * kThreads, c = (i >> 5) % (W / 4), tile = (i >> 5) / (W / 4);
-      const __nv_bfloat16* qr = query_row(p, s, hk, r0 + 8 * tile + g);
-      v[k] = query8<DT>(i < all ? qr : nullptr, R::dim(c, t));
+      const int tile = tile0 + k * kWarps;
+      const __nv_bfloat16* qr = 8 * tile < n ? query_row(p, s, hk, r0 + 8 * tile + g) : nullptr;
+#pragma unroll
+      for (int c = 0; c < W / 4; ++c) v[k][c] = query8(qr, R::dim(c, t));
+    }
+    for (int i = threadIdx.x; i < L::kRows; i += kThreads) {
+      float* row = reinterpret_cast<float*>(&s_row[i >> 1]) + (i & 1);
+      row_info(p, s, hk, r0 + i, row[0], s_lim[i]);
+      if constexpr (DT == PKV_BF16) row[2] = sl2;
     }
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) qs[threadIdx.x + k * kThreads] = v[k];
-    for (int i = threadIdx.x; i < L::kRows; i += kThreads) row_info(p, s, hk, r0 + i, s_l2[i], s_lim[i]);
+    for (int k = 0; k < kEach; ++k) {
+      const int tile = tile0 + k * kWarps;
+      if constexpr (DT != PKV_BF16) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < W / 4; ++c) most = most8(v[k][c], most);
+        const RowScale scale(most_of_row(most));
+#pragma unroll
+        for (int c = 0; c < W / 4; ++c) v[k][c] = f16x8(v[k][c], scale);
+        if (t == 0) reinterpret_cast<float*>(&s_row[4 * tile + (g >> 1)])[2 + (g & 1)] = sl2 * scale.down();
+      }
+#pragma unroll
+      for (int c = 0; c < W / 4; ++c) qs[(tile * (W / 4) + c) * 32 + lane] = v[k][c];
+    }
   };
   const bool once = s.rows <= L::kRows;
   if (once) {
@@ -459,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
           const uint4 v = qs[(j * (W / 4) + c) * 32 + lane];
           qw[4 * c] = v.x, qw[4 * c + 1] = v.y, qw[4 * c + 2] = v.z, qw[4 * c + 3] = v.w;
         }
-        const float2 l2 = *reinterpret_cast<const float2*>(&s_l2[8 * j + 2 * t]);
+        const float4 row = s_row[4 * j + t];
         const int2 lim = *reinterpret_cast<const int2*>(&s_lim[8 * j + 2 * t]);
         float c[MT][4];
 #pragma unroll
@@ -473,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int key = t0 + 16 * x + 8 * h + g;
-            const float w0 = ex2(fmaf(c[x][2 * h], sl2, -l2.x)), w1 = ex2(fmaf(c[x][2 * h + 1], sl2, -l2.y));
+            const float w0 = ex2(fmaf(c[x][2 * h], row.z, -row.x)), w1 = ex2(fmaf(c[x][2 * h + 1], row.w, -row.y));
             sum[x][h] += key < lim.x ? w0 : 0.f;
             sum[x][h] += key < lim.y ? w1 : 0.f;
           }

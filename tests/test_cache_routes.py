@@ -153,6 +153,27 @@ def test_rows_of_different_magnitudes_in_one_tile(pkv, d, hq):
     check(cache, want[0], want[1], clean, lq, lens, True)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("d,hq,lq", [(64, 8, 1), (128, 16, 1), (256, 8, 1), (64, 16, 40), (128, 8, 300), (256, 4, 40)])
+@pytest.mark.parametrize("power", [-100, -20, 20, 100])
+def test_weights_of_queries_of_any_magnitude(pkv, dtype, d, hq, lq, power):
+    lens = [400, 65]
+    cache = LC.Cache(87, dtype=dtype, lens=lens, hkv=1, d=d, page=16)
+    g = torch.Generator().manual_seed(8)
+    q = (1.5 * torch.randn(2 * lq, hq, d, generator=g)).bfloat16().cuda()
+    lse = torch.cat([f[1] for f in LC.attention(cache, q, [lq] * 2, lens, True)], 1).float().contiguous()
+    status, found = torch.zeros(3, dtype=torch.int32, device="cuda"), []
+    for x in (0, power):
+        prob = cache.problem(pkv, hq, True, d ** -0.5 * 2.0 ** -x)
+        qx = (q.double() * 2.0 ** x).bfloat16()
+        scores = torch.zeros(2, 1, 400, device="cuda")
+        args = cache.args(pkv, q=qx, lse=lse, cu_seqlens_q=LC.i32([0, lq, 2 * lq]), max_seqlen_q=lq)
+        pkv.attn_weights(prob, args, pkv.make_weights_args(scores=scores, max_seqlen_k=400), status)
+        found.append(scores)
+    assert status.tolist() == [0, 0, 0] and torch.equal(*found)
+
+
 # ------------------------------------------------------------------ the bytes of the copies
 def kinds_of(pkv, lq, lens, hq, hkv, d):
     prob = pkv.make_problem(batch=len(lq), num_heads_q=hq, num_heads_kv=hkv, head_dim=d, page_size=64,
