@@ -312,7 +312,9 @@ pkv_status pkv_plan_get_items(pkv_plan_t plan, pkv_work_item* h_items, int32_t c
  * attends the first cache_seqlens[b] + new_len[b] keys of its sequence.
  * cache_seqlens itself is NOT advanced (the caller does that).  Launches the
  * append (if any), one persistent attention kernel and, when a unit was
- * split, one combine kernel; no host synchronisation and no allocation.
+ * split, one combine kernel; over an fp4 cache the attention (and combine) of the
+ * tiles straight over it, and then, for sequences over copies, the copying kernel,
+ * the persistent kernel and its combine.  No host synchronisation and no allocation.
  * The plan must have been made from the same lengths and uploaded into
  * `workspace`.
  */
@@ -559,8 +561,9 @@ const char* pkv_last_error(void);
 /* Timing hook for benchmarks: when start/stop are non-NULL (cudaEvent_t
  * passed as void*), every later pkv_attn_varlen_kvcache_fwd on this host
  * thread records `start` immediately before and `stop` immediately after the
- * persistent attention kernel (the first and the last of them, where a call
- * launches two), on the call's stream.  NULL, NULL turns it off.
+ * persistent attention kernel, on the call's stream (where a call over an fp4 cache
+ * launches two: before the first, and after the last; what copies rows for one
+ * counts as part of it).  NULL, NULL turns it off.
  * A call captured into a CUDA graph records them as event-record nodes, so each
  * replay of the graph re-records them.  The events stay owned by the caller. */
 pkv_status pkv_set_profile_events(void* start_event, void* stop_event);

@@ -615,7 +615,11 @@ pkv_status run_far(const pkv_problem& pr, const pkv_fwd_args* args, pkv_plan_t p
   g.c_stride_head = args->kc_stride_head;
   g.sf = fp4_scales(args);
   g.status = status;
-  cudaError_t e = launch_gather(g, pr.cache_dtype, s);
+  // (where no launch before has been timed, the copies are the first that is)
+  cudaError_t e;
+  if (g_ev_start && (e = record_profile_event(g_ev_start, s)) != cudaSuccess) return cuda_fail(e, "profile event");
+  g_ev_start = nullptr;
+  e = launch_gather(g, pr.cache_dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "kv_gather launch");
 
   // rows where cu_seqlens_q says: the other sequences' lie between these
@@ -626,8 +630,8 @@ pkv_status run_far(const pkv_problem& pr, const pkv_fwd_args* args, pkv_plan_t p
   return run_attention(far->problem, &a, far, ws + F.plan, status, args->k_scale, args->v_scale, false, false, s);
 }
 
-// The profiling events of a call with two attention launches: no stop after the first, no
-// start before the second (where the first has items); put back at the end.
+// The profiling events of a call with two attention launches: no stop after the first, one
+// start, before the first that has items (the copies belong to the second); put back at the end.
 struct ProfileEvents {
   cudaEvent_t start = g_ev_start, stop = g_ev_stop;
   bool first;

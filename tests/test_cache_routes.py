@@ -1,11 +1,14 @@
 """Attention over a 4-bit cache by either route, tiles straight over its rows and tensor-core tiles over copies of them:
 the same answers, the same precision, over the whole range of its inputs."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from tests import long_cache as LC
 from tests.test_fp4 import attend, check
+from tests.test_stream_order import _EdgeData
 
 
 @pytest.fixture(scope="module")
@@ -220,3 +223,61 @@ def test_prompts_without_a_workspace(pkv):
     args.keep[5][0] -= 1  # lengths other than the plan's
     pkv.attn_varlen_kvcache_fwd_noalloc(prob, args, plan)
     assert pkv.get_status_noalloc() == 7
+
+
+# ------------------------------------------------------------------ profiling events
+def nodes_of(call):
+    """Captures a call: its nodes in order, each "kernel" or "event" (they form a chain)."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    stream = torch.cuda.Stream()
+    graph, n = ctypes.c_void_p(), ctypes.c_size_t()
+    handle = ctypes.c_void_p(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        assert cu.cuStreamBeginCapture_v2(handle, 2) == 0  # (relaxed)
+        call(stream)
+        assert cu.cuStreamEndCapture(handle, ctypes.byref(graph)) == 0
+    root = (ctypes.c_void_p * 1)()
+    assert cu.cuGraphGetRootNodes(graph, None, ctypes.byref(n)) == 0 and n.value == 1
+    assert cu.cuGraphGetRootNodes(graph, root, ctypes.byref(n)) == 0
+    assert cu.cuGraphGetEdges_v2(graph, None, None, None, ctypes.byref(n)) == 0
+    a, b, data = (ctypes.c_void_p * n.value)(), (ctypes.c_void_p * n.value)(), (_EdgeData * n.value)()
+    assert cu.cuGraphGetEdges_v2(graph, a, b, data, ctypes.byref(n)) == 0
+    after, at, found = dict(zip(a, b)), root[0], []
+    assert len(after) == n.value
+    while at is not None:
+        kind = ctypes.c_int()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(at), ctypes.byref(kind)) == 0
+        found.append({0: "kernel", 7: "event"}[kind.value])
+        at = after.get(at)
+    assert cu.cuGraphDestroy(graph) == 0
+    return found
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,lq,new,kinds", [
+    ([900, 513], [700, 300], [0, 0], {1}), ([900, 513], [700, 300], [700, 0], {1}), ([900, 50], [700, 1], [0, 1], {0, 1}),
+    ([900, 50], [1, 1], [1, 1], {0}),
+])
+def test_profiling_events_go_around_the_copies(pkv, lens, lq, new, kinds):
+    """The start event stands behind the append and before everything else, the copies of prompts among it, whether or not
+    tiles straight over the cache come first; the stop event behind the last attention launch."""
+    cache = LC.Cache(89, dtype="fp4", lens=lens, hkv=4, d=128, page=16)
+    q, out, lse, plan, ws, args, prob = attend(pkv, cache, 16, lq, new)
+    assert {it["kind"] for it in plan.items()} == kinds
+    call = lambda s: pkv.attn_varlen_kvcache_fwd(prob, args, plan, ws, stream=s)
+    plain = nodes_of(call)
+    assert set(plain) == {"kernel"}
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+    a.record(), b.record()
+    torch.cuda.synchronize()
+    pkv.set_profile_events(a, b)
+    try:
+        found = nodes_of(call)
+    finally:
+        pkv.set_profile_events(None, None)
+    assert found.count("event") == 2 and [k for k in found if k == "kernel"] == plain
+    start = found.index("event")
+    assert start == (1 if sum(new) else 0)                    # behind the append
+    behind = found[found.index("event", start + 1) + 1:]
+    assert len(behind) <= 1                                   # a combine at most
+    assert plain == nodes_of(call)
