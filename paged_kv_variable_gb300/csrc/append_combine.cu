@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
       acc[4] += w * b.x; acc[5] += w * b.y; acc[6] += w * b.z; acc[7] += w * b.w;
     }
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-    const int tok = (p.q_offsets != nullptr ? __ldg(p.q_offsets + ci.b) : ci.q_row0) + row / ci.nh;
+    const int tok = (p.q_offsets != nullptr ? __ldg(p.q_offsets + ci.b) + ci.q_i0 : ci.q_row0) + row / ci.nh;
     const int head = ci.hk * p.G + ci.h0 + row % ci.nh;
     uint4 v;
     v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(32 * kSharedCombineWarps) combine_shared_kerne
       for (int i = 0; i < E; ++i) acc[i] += sums[k][lane * E + i];
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  const int out_row = (p.q_offsets != nullptr ? __ldg(p.q_offsets + ci.b) : ci.q_row0) + tok;
+  const int out_row = (p.q_offsets != nullptr ? __ldg(p.q_offsets + ci.b) + ci.q_i0 : ci.q_row0) + tok;
   const int head = ci.hk * p.G + ci.h0 + g;
   __nv_bfloat16* dst = p.out + (int64_t)out_row * p.o_stride_tok + (int64_t)head * p.o_stride_head + lane * E;
   if constexpr (E == 2) {

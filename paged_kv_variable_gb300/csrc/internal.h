@@ -97,7 +97,7 @@ static_assert(sizeof(WorkItem) == 64, "WorkItem layout");
 // rows [0, n_q * nh) starting at partial slot slot0 + s * slot_stride.
 struct CombineItem {
   int32_t b;            // sequence
-  int32_t q_row0;       // its first query row when rows are packed (else cu_seqlens_q[b])
+  int32_t q_row0;       // its first query row when rows are packed (else cu_seqlens_q[b] + q_i0)
   int32_t n_q;
   int32_t hk;
   int32_t nsplit;
@@ -109,7 +109,7 @@ struct CombineItem {
   // apart from p_slot0, each of tiles of p_tile_slots slots holding p_tq tokens;
   // this unit's first token is token p_tok0 of the sequences sharing the prefix
   int32_t p_nsplit, p_slot0, p_chunk_slots, p_tq, p_tile_slots, p_tok0;
-  int32_t pad;
+  int32_t q_i0;         // its first query token within the sequence
 };
 static_assert(sizeof(CombineItem) == 64, "CombineItem layout");
 

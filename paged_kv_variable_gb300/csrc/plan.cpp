@@ -508,6 +508,7 @@ pkv_status make_fp4_plan(const pkv_problem& p, const int32_t* h_q_lens, const in
             CombineItem ci{};
             ci.b = b;
             ci.q_row0 = w.q_row0;
+            ci.q_i0 = i0;
             ci.n_q = w.n_q;
             ci.hk = hk;
             ci.nsplit = n;

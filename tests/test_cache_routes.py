@@ -281,3 +281,50 @@ def test_profiling_events_go_around_the_copies(pkv, lens, lq, new, kinds):
     behind = found[found.index("event", start + 1) + 1:]
     assert len(behind) <= 1                                   # a combine at most
     assert plain == nodes_of(call)
+
+
+# ------------------------------------------------------------------ rows placed by the caller
+def placed(pkv, cache, hq, lq, starts, rows, *, dynamic=False, causal=True):
+    """The same call with packed rows and with rows at `starts` of `rows`, the others NaN."""
+    g = torch.Generator().manual_seed(9)
+    q = (1.5 * torch.randn(sum(lq), hq, cache.d, generator=g)).bfloat16().cuda()
+    at = np.concatenate([np.arange(s, s + n) for s, n in zip(starts, lq)])
+    q2 = torch.full((rows, hq, cache.d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q2[at] = q
+    prob, found = cache.problem(pkv, hq, causal), []
+    plan = (pkv.plan_decode_dynamic if dynamic else pkv.plan)(prob, lq, cache.lens)
+    ws = pkv.workspace_tensor(plan.workspace_bytes)
+    for x, cu, kw in ((q, np.cumsum([0] + lq), {}), (q2, starts + [rows], dict(q_rows=rows))):
+        out = torch.full_like(x, 7.0)
+        lse = torch.full((hq, x.shape[0]), 7.0, device="cuda")
+        plan.upload(ws)
+        args = cache.args(pkv, q=x, out=out, lse=lse, cu_seqlens_q=LC.i32(cu), max_seqlen_q=max(lq), **kw)
+        pkv.attn_varlen_kvcache_fwd(prob, args, plan, ws)
+        assert pkv.get_status(ws) == 0
+        found.append((out, lse))
+    (out, lse), (out2, lse2) = found
+    check(cache, out, lse, q, lq, cache.lens, causal)
+    assert torch.equal(out2[at], out) and torch.equal(lse2[:, at], lse)
+    left = np.setdiff1d(np.arange(rows), at)
+    assert bool((out2[left] == 7).all()) and bool((lse2[:, left] == 7).all())
+    return plan
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq,hkv", [(64, 64, 4), (128, 32, 4), (256, 16, 4)])
+@pytest.mark.parametrize("dynamic", [False, True])
+def test_placed_rows_of_split_runs(pkv, d, hq, hkv, dynamic):
+    """Runs of more than one tile whose keys are split: the parts of a later tile are joined into its own rows."""
+    cache = LC.Cache(71, dtype="fp4", lens=[9011, 5000, 30], hkv=hkv, d=d, page=16)
+    plan = placed(pkv, cache, hq, [5, 4, 3], [11, 2, 20], 24, dynamic=dynamic)
+    split = {it["q_index0"] for it in plan.items() if it["partial_slot"] >= 0}
+    assert len(split) > 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq,hkv", [(128, 16, 4), (256, 8, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_placed_rows_of_prompts(pkv, d, hq, hkv, causal):
+    cache = LC.Cache(72, dtype="fp4", lens=[900, 50, 1537], hkv=hkv, d=d, page=16)
+    plan = placed(pkv, cache, hq, [700, 1, 300], [350, 3, 20], 1100, causal=causal)
+    assert {it["kind"] for it in plan.items()} == {0, 1}
