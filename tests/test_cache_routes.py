@@ -9,6 +9,7 @@ import torch
 from tests import long_cache as LC
 from tests.test_fp4 import attend, check
 from tests.test_stream_order import _EdgeData
+from tests.test_weights import run_evict, run_weights
 
 
 @pytest.fixture(scope="module")
@@ -328,3 +329,16 @@ def test_placed_rows_of_prompts(pkv, d, hq, hkv, causal):
     cache = LC.Cache(72, dtype="fp4", lens=[900, 50, 1537], hkv=hkv, d=d, page=16)
     plan = placed(pkv, cache, hq, [700, 1, 300], [350, 3, 20], 1100, causal=causal)
     assert {it["kind"] for it in plan.items()} == {0, 1}
+
+
+# ------------------------------------------------------------------ long sequences
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq,lq", [(64, 6, 3), (128, 4, 1), (128, 16, 40)])
+def test_long_documents(pkv, d, hq, lq):
+    """131072 keys and a few more, by tiles of few rows and of 128: attention, the keys' weights, an eviction."""
+    lens = [131072 + 77]
+    cache = LC.Cache(73, dtype="fp4", lens=lens, hkv=1, d=d, page=64, head_major=True)
+    attend(pkv, cache, hq, [lq], [min(lq, 2)])
+    run_weights(pkv, cache, hq, [lq])
+    scores = torch.rand(1, 1, lens[0], generator=torch.Generator().manual_seed(d)).cuda()
+    run_evict(pkv, cache, scores, [8200], 4, 1000)
