@@ -48,7 +48,7 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t v) {
 }
 
 // A query row in bf16 as f16 operands: times the power of two that brings its largest magnitude
-// to [2^14, 2^15) (2^126 at most), so that any row keeps its bits but for dims that are 2^-28 of
+// to [2^14, 2^15) (2^126 at most), so that any row keeps its bits but for dims that are 2^-31 of
 // that or less; its logits take the inverse.
 struct RowScale {
   uint32_t up;  // biased exponent

@@ -21,10 +21,12 @@
 // sums and O are fp32; P is rounded to f16 (11 bits), kept above the subnormals
 // by a factor 64.
 //
-// Instructions bound it, about 635 of a warp for 32 keys at head_dim 128, most of them
-// conversions, products with the scales and the interleave, at two cycles each on
-// their pipes: 64 sequences of 512 to 4096 keys (8 kv heads, 166 MB) 45 us with the combine,
-// 57% of the issue slots; two of 131072 keys 65 us (4.6 TB/s).
+// About 635 instructions of a warp for 32 keys at head_dim 128, most of them conversions,
+// products with the scales and the interleave.  No unit is near its limit (64 sequences of 512
+// to 4096 keys, 8 kv heads, 166 MB: issue slots 57%, ALU 47%, DRAM 53%, FMA 33%, warp MMAs
+// 22%): a step is a chain of them, and four warps a scheduler, what the registers allow, wait
+// for one another's results (1.6 warps at a fixed latency for each issue).  45 us with the
+// combine; two sequences of 131072 keys 64.5 us (4.7 TB/s).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -218,7 +220,6 @@ __global__ void __launch_bounds__(kThreads, fp4_blocks(D, 8 * NQ))
                      vl - prow * p.c_stride_tok, ks, vs, k_dst + st, v_dst + st, s_dst + st, pdiv);
     }
   };
-  grid_dep_wait();  // the append, where this launch overlaps it
   constexpr int kNext = kWarps * kStep;               // keys between a warp's steps
   const int key0 = w.kv_begin + warp * kStep + lane;  // this lane's key of its first step
   int pg = load_page(key0);

@@ -14,7 +14,8 @@
 //
 // Many rows (a window of queries, a prompt): the keys of a step stay in registers and
 // the queries pass by from shared memory, where the block puts them in the order of
-// the MMA's operand (128 rows at a time).  The warp MMAs and exponentials bound it: 32
+// the MMA's operand (128 rows at a time).  The warp MMAs (their pipe is in use 53% of the
+// time) and the chain MMA, exponential, sum of a tile bound it: 32
 // queries a sequence of 8 prompts of 5000 to 16384 fp8 keys, 128 rows a kv head, 76.0 us, of
 // which the MMAs at their rate would take 37.  (The same with S^T = K Q^T by tcgen05 MMAs, a key
 // a thread, the queries staged as operands (an fp8 one as two e4m3 terms): 88 us, for the
