@@ -614,6 +614,7 @@ pkv_status run_far(const pkv_problem& pr, const pkv_fwd_args* args, pkv_plan_t p
   g.c_stride_tok = args->kc_stride_tok;
   g.c_stride_head = args->kc_stride_head;
   g.sf = fp4_scales(args);
+  g.k_scale = args->k_scale;
   g.status = status;
   // (where no launch before has been timed, the copies are the first that is)
   cudaError_t e;

@@ -38,6 +38,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cfloat>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -1169,7 +1170,6 @@ __device__ bool softmax_item(const AttnParams& p, const WorkItem& w, uint8_t* sm
   }
   const int n = num_tiles<L::kTile>(w);
   float m = -INFINITY, l = 0.f;
-
   for (int j = 0; j < n; ++j) {
     const uint32_t T = pt + j;
     const int t0 = w.kv_begin + j * kTile;
@@ -1973,7 +1973,9 @@ __device__ bool consumer(const AttnParams& p, uint8_t* smem, const Bars& B, vola
   }
   const float kscale = FP8 || R4 ? __ldg(p.k_scale) : 1.f;
   const float vscale = FP8 || R4 ? __ldg(p.v_scale) : 1.f;
-  const float sl2 = p.scale_log2 * kscale;
+  // (R4: the keys' copies carry the sign of their scale, as the largest product has to be the
+  // largest logit; and with a scale of 0 masked logits stay apart from the others)
+  const float sl2 = R4 ? fmaxf(p.scale_log2 * fabsf(kscale), FLT_MIN) : p.scale_log2 * kscale;
   // quantised queries: S = codes(Q) . codes(K), times q_scale and k_scale
   const float sl2q = (FP8 && p.q_scale) ? sl2 * __ldg(p.q_scale) : sl2;
   Ring rk, rv;

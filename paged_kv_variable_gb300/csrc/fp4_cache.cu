@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kRowThreads) fp4_append_kernel(const AppendPar
 
 // ------------------------------------------------------------------ gather
 // A block of 16 dims, key or value: 32, 16 or 8 + 1 bytes in, 32 out (f16: code x block scale
-// as f16, without the tensor's scale).
+// as f16, without the tensor's scale; of the copies that an attention reads the keys have its
+// sign alone).
 template <int DT>
 __device__ __forceinline__ void read16(const void* cache, const uint8_t* sf, float scale, bool f16, uint32_t* w) {
   uint32_t h[8];
@@ -285,7 +286,8 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherParams 
     const uint8_t* sf = (x == 0 ? p.sf.k : p.sf.v) + sat;
     const float* scale = x == 0 ? p.k_scale : p.v_scale;
     if ((x == 0 ? p.k_out : p.v_out) == nullptr) continue;
-    const float f = scale != nullptr ? __ldg(scale) : 1.f;
+    float f = scale != nullptr ? __ldg(scale) : 1.f;
+    if (p.lens != nullptr) f = f < 0.f ? -1.f : 1.f;
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
       if constexpr (DT == PKV_BF16)

@@ -342,3 +342,17 @@ def test_long_documents(pkv, d, hq, lq):
     run_weights(pkv, cache, hq, [lq])
     scores = torch.rand(1, 1, lens[0], generator=torch.Generator().manual_seed(d)).cuda()
     run_evict(pkv, cache, scores, [8200], 4, 1000)
+
+
+# ------------------------------------------------------------------ scales of any sign
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq,hkv", [(64, 32, 4), (128, 16, 4), (256, 8, 2)])
+@pytest.mark.parametrize("k_scale", [-0.07, -2.0, 0.0])
+def test_key_scales_below_zero_and_of_zero(pkv, d, hq, hkv, k_scale):
+    """Both routes order the logits, not the sums of products: a tensor scale below 0, and of 0 (all keys alike)."""
+    lens, lq = [700, 900, 300], [1, 700, 4]
+    cache = LC.Cache(74, dtype="fp4", lens=lens, hkv=hkv, d=d, page=16)
+    cache.k_scale = k_scale
+    cache.scales[0].fill_(k_scale)
+    plan = attend(pkv, cache, hq, lq, [0] * 3)[3]
+    assert {it["kind"] for it in plan.items()} == {0, 1}
